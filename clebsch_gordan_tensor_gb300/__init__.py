@@ -27,7 +27,7 @@ LIB_PATH = os.path.join(_HERE, "_build", "libcgtp.so")
 _lock = threading.Lock()
 _lib = None
 
-F32, F64 = 0, 1
+F32, F64, BF16, F16 = 0, 1, 2, 3
 W_PER_EDGE, W_SHARED = 0, 1
 WEIGHTS_BF16 = 1 << 24  # plan flag: weights stored as bfloat16
 WEIGHTS_F16 = 1 << 25  # plan flag: weights stored as IEEE binary16
@@ -41,6 +41,20 @@ class CgtpError(RuntimeError):
 
 class _LinInstr(ctypes.Structure):
     _fields_ = [("i_in", ctypes.c_int), ("i_out", ctypes.c_int)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64)]
+
+
+class _AdamwTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("numel", ctypes.c_int64)]
+
+
+class _AdamwArgs(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("step", ctypes.c_int64), ("seed", ctypes.c_uint64)]
 
 
 class _Instr(ctypes.Structure):
@@ -134,6 +148,28 @@ def lib() -> ctypes.CDLL:
                 "cgtp_uvw_conv_backward": [vp, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp,
                                            ctypes.c_double, vp, vp, vp, vp, vp, vp,
                                            ctypes.c_size_t, vp],
+                "cgtp_embed_forward": [i32, i32, i64, i64, i64, vp, vp, ctypes.c_double, vp, i64,
+                                       vp],
+                "cgtp_embed_backward": [i32, i32, i64, i64, i64, vp, vp, i64, ctypes.c_double, vp,
+                                        vp, ctypes.c_size_t, vp],
+                "cgtp_embed_backward_workspace": [i32, i64, i64, i64, P(ctypes.c_size_t)],
+                "cgtp_embed_device_status": [P(i32)],
+                "cgtp_norm_create": [P(vp), ctypes.c_char_p, ctypes.c_double, i32],
+                "cgtp_norm_destroy": [vp],
+                "cgtp_norm_info": [vp, P(i64), P(i64)],
+                "cgtp_norm_workspace": [vp, P(ctypes.c_size_t)],
+                "cgtp_norm_forward": [vp, i64, _Rows, vp, _Rows, vp],
+                "cgtp_norm_backward": [vp, i64, _Rows, vp, _Rows, _Rows, vp, vp, ctypes.c_size_t,
+                                       vp],
+                "cgtp_residual_forward": [vp, i64, _Rows, _Rows, vp, _Rows, vp, vp, _Rows, _Rows,
+                                          vp],
+                "cgtp_residual_backward": [vp, i64, _Rows, _Rows, vp, _Rows, vp, vp, _Rows, _Rows,
+                                           _Rows, _Rows, _Rows, vp, vp, vp, vp, ctypes.c_size_t,
+                                           vp],
+                "cgtp_adamw_layout": [i32, P(i64), P(i64), P(i64)],
+                "cgtp_adamw_step": [i32, i32, i32, i32, P(_AdamwTensor), vp, vp, vp, vp, vp, i32,
+                                    P(_AdamwArgs), vp],
+                "cgtp_adamw_values": [i64, vp, vp, vp, vp, i32, vp, vp, vp],
             }
             for name, args in sig.items():
                 f = getattr(L, name)
@@ -771,3 +807,6 @@ def _Borrowed(cls, handle, owner):
     obj._h = handle
     obj._borrowed = True
     return obj
+
+
+from .train import AdamW, IrrepsNorm, embed_backward, embed_device_status, embed_forward  # noqa: E402,F401

@@ -1,0 +1,375 @@
+// AdamW over many tensors at once (sm_103a), with 32-bit moments (64-bit for
+// fp64 parameters) or moments held in 8 bits.
+//
+//   m = b1 m + (1 - b1) g          v = b2 v + (1 - b2) g^2
+//   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v / (1 - b2^t)) + eps)
+//
+// One launch covers up to kMaxTensors tensors: their addresses and lengths
+// travel as a kernel parameter, the states of all tensors lie one after another
+// in flat arrays, each tensor starting on a block of 256 elements, and one warp
+// takes one block at a time.
+//
+// 8-bit moments.  m has a sign, 4 exponent and 3 fraction bits, v 5 exponent
+// and 3 fraction bits (gradual underflow in both), and one power of two per
+// block and moment puts the block's largest value in the top binade.  Powers of
+// two make the scaling exact, so a value that is on the grid stays what it was.
+// The grid's relative step is 1/8 to 1/16 and one step of beta2 = 0.999 moves v
+// by 1/1000: rounding to nearest would never move it.  So values are rounded up
+// or down with the probability of their distance, by 16 bits of a hash of
+// (seed, step, tensor, element), which keeps the mean of the recursion exact
+// and the result reproducible.  v reaches down to 2^-34 of the block's power of
+// two (sqrt: 2^-17) and a positive v never rounds to zero; m's smallest value,
+// 2^-18, lies below sqrt of the smallest v, so no element's m / sqrt(v) is
+// blown up by the formats.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "internal.hpp"
+#include "storage.cuh"
+
+namespace cgtp {
+
+namespace {
+
+constexpr int kMaxTensors = 64;  // per launch: a 2 KB table in the kernel's parameters
+constexpr int kBlock = kAdamwBlock;
+constexpr int kWarps = 8;
+
+struct AdamwEntry {
+    void* p;
+    const void* g;
+    int64_t numel;
+    uint32_t block0;  // first block in this launch
+    uint32_t key;     // of the rounding hash
+};
+
+struct AdamwTable {
+    AdamwEntry t[kMaxTensors];
+    int n;
+    uint32_t blocks;
+};
+
+template <typename C>
+struct AdamwScalars {
+    C b1, c1, b2, c2, keep, rate, root, eps;
+};
+
+// Finaliser of MurmurHash3's 32-bit variant (A. Appleby, public domain).
+__host__ __device__ __forceinline__ uint32_t mix32(uint32_t h) {
+    h = (h ^ (h >> 16)) * 0x85EBCA6Bu;
+    h = (h ^ (h >> 13)) * 0xC2B2AE35u;
+    return h ^ (h >> 16);
+}
+
+// 2^(byte - 128); 0 for the byte of a fresh (zero-filled) state, NaN for 255,
+// the mark of a block that holds an infinity or a NaN.
+__device__ __forceinline__ float block_scale(uint32_t byte) {
+    const uint32_t b = byte > 1u ? (byte - 1u) << 23 : 0u;
+    return __uint_as_float(byte == 255u ? 0x7FC00000u : b);
+}
+
+// Exponent byte of a block whose largest magnitude has the given fp32 bits.
+__device__ __forceinline__ int block_exponent(uint32_t top) {
+    return min(max((int)(top >> 23) - 126, -80), 126);
+}
+
+// sign, 4 exponent, 3 fraction bits; the exponent field of 2^111 times the
+// value is the code's own, so encoding is a shift of the fp32 bits.
+__device__ __forceinline__ float decode_m(uint32_t c, float scale) {
+    const float a = __uint_as_float((c & 0x7Fu) << 20) * 0x1p111f * scale;
+    return __uint_as_float(__float_as_uint(a) | (c & 0x80u) << 24);
+}
+__device__ __forceinline__ uint32_t encode_m(float x, float inv, uint32_t noise) {
+    const uint32_t y = __float_as_uint(__fmul_rn(__fmul_rn(fabsf(x), inv), 0x1p-111f));
+    return min((y + noise) >> 20, 127u) | (__float_as_uint(x) >> 24 & 0x80u);
+}
+__device__ __forceinline__ float decode_v(uint32_t c, float scale) {
+    return __uint_as_float(c << 20) * 0x1p95f * scale;
+}
+__device__ __forceinline__ uint32_t encode_v(float x, float inv, uint32_t noise) {
+    const uint32_t y = __float_as_uint(__fmul_rn(__fmul_rn(x, inv), 0x1p-95f));
+    return max(min((y + noise) >> 20, 255u), x > 0.f ? 1u : 0u);
+}
+
+// The moments' recursions keep their two products apart (no fused multiply-add):
+// the stochastic rounding that follows compares against exact thresholds, and
+// this is the form that other implementations reproduce bit for bit.
+__device__ __forceinline__ float ema(float s, float b, float x, float c) {
+    return __fadd_rn(__fmul_rn(s, b), __fmul_rn(x, c));
+}
+__device__ __forceinline__ double ema(double s, double b, double x, double c) {
+    return __dadd_rn(__dmul_rn(s, b), __dmul_rn(x, c));
+}
+__device__ __forceinline__ float square(float x) { return __fmul_rn(x, x); }
+__device__ __forceinline__ double square(double x) { return __dmul_rn(x, x); }
+
+// The step itself needs no exact rounding: a few units in the last place of
+// m / sqrt(v) move p by lr times that.
+__device__ __forceinline__ float stepped(float p, float m, float v, const AdamwScalars<float>& a) {
+    float r;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return p * a.keep - a.rate * __fdividef(m, r * a.root + a.eps);
+}
+__device__ __forceinline__ double stepped(double p, double m, double v,
+                                          const AdamwScalars<double>& a) {
+    return p * a.keep - a.rate * (m / (sqrt(v) * a.root + a.eps));
+}
+
+// copy_kind: 0 none, 1 bfloat16, 2 binary16.
+template <typename P, typename G, bool EIGHT>
+__global__ void __launch_bounds__(32 * kWarps)
+adamw_kernel(const __grid_constant__ AdamwTable tab,
+             const AdamwScalars<typename Compute<P>::type> a, void* __restrict__ m_,
+             void* __restrict__ v_, uint8_t* __restrict__ m_exp, uint8_t* __restrict__ v_exp,
+             uint16_t* __restrict__ copy, int copy_kind) {
+    using C = typename Compute<P>::type;
+    constexpr int V = sizeof(C) == 8 ? 2 : 4;  // elements of one access
+    constexpr int NV = kBlock / 32 / V;        // accesses of a lane
+    const int lane = threadIdx.x & 31;
+    const uint32_t warps = gridDim.x * kWarps;
+    for (uint32_t b = blockIdx.x * kWarps + (threadIdx.x >> 5); b < tab.blocks; b += warps) {
+        int lo = 0, hi = tab.n - 1;  // the last tensor that starts at or before block b
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (tab.t[mid].block0 <= b)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const AdamwEntry& e = tab.t[lo];
+        const int64_t first = (int64_t)(b - e.block0) * kBlock;
+        P* p = static_cast<P*>(e.p) + first;
+        const G* g = static_cast<const G*>(e.g) + first;
+        const int64_t left = e.numel - first;
+        const int64_t at = (int64_t)b * kBlock;
+        const bool whole = left >= kBlock && (uintptr_t)p % (sizeof(P) * V) == 0 &&
+                           (uintptr_t)g % (sizeof(G) * V) == 0;
+        Pack<P, V> pp[NV];
+        C gg[NV][V], m[NV][V], v[NV][V];
+        if (whole) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                pp[j] = load_pack<P, V>(p + (j * 32 + lane) * V);
+                const Pack<G, V> gp = load_pack<G, V>(g + (j * 32 + lane) * V);
+#pragma unroll
+                for (int i = 0; i < V; ++i) gg[j][i] = (C)widen(gp.v[i]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int k = (j * 32 + lane) * V + i;
+                    pp[j].v[i] = k < left ? p[k] : narrow<P>((C)0);
+                    gg[j][i] = k < left ? (C)widen(g[k]) : (C)0;
+                }
+        }
+        if constexpr (EIGHT) {
+            const float ms = block_scale(m_exp[b]), vs = block_scale(v_exp[b]);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int64_t k = at + (j * 32 + lane) * V;
+                const uint32_t mc = *reinterpret_cast<const uint32_t*>((uint8_t*)m_ + k);
+                const uint32_t vc = *reinterpret_cast<const uint32_t*>((uint8_t*)v_ + k);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    m[j][i] = decode_m(mc >> 8 * i & 0xFFu, ms);
+                    v[j][i] = decode_v(vc >> 8 * i & 0xFFu, vs);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int64_t k = at + (j * 32 + lane) * V;
+                const Pack<C, V> mp = load_pack<C, V>((C*)m_ + k), vp = load_pack<C, V>((C*)v_ + k);
+#pragma unroll
+                for (int i = 0; i < V; ++i) m[j][i] = mp.v[i], v[j][i] = vp.v[i];
+            }
+        }
+        uint32_t mtop = 0, vtop = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                m[j][i] = ema(m[j][i], a.b1, gg[j][i], a.c1);
+                v[j][i] = ema(v[j][i], a.b2, square(gg[j][i]), a.c2);
+                const C pn = stepped((C)widen(pp[j].v[i]), m[j][i], v[j][i], a);
+                pp[j].v[i] = narrow<P>(pn);
+                if constexpr (EIGHT) {
+                    mtop = max(mtop, __float_as_uint(m[j][i]) & 0x7FFFFFFFu);
+                    vtop = max(vtop, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
+                }
+            }
+        }
+        if (whole) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) store_pack(p + (j * 32 + lane) * V, pp[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int k = (j * 32 + lane) * V + i;
+                    if (k < left) p[k] = pp[j].v[i];
+                }
+        }
+        if (copy_kind != 0) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                Pack<uint16_t, V> c;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float x = (float)widen(pp[j].v[i]);
+                    c.v[i] = copy_kind == 1 ? __bfloat16_as_ushort(__float2bfloat16_rn(x))
+                                            : __half_as_ushort(__float2half_rn(x));
+                }
+                store_pack(copy + at + (j * 32 + lane) * V, c);
+            }
+        }
+        if constexpr (EIGHT) {
+            mtop = __reduce_max_sync(0xFFFFFFFFu, mtop);
+            vtop = __reduce_max_sync(0xFFFFFFFFu, vtop);
+            const int me = block_exponent(mtop), ve = block_exponent(vtop);
+            const float mi = __uint_as_float((uint32_t)(127 - me) << 23);
+            const float vi = __uint_as_float((uint32_t)(127 - ve) << 23);
+            const uint32_t key = mix32(e.key + (uint32_t)((uint64_t)first >> 32));
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                uint32_t mc = 0, vc = 0;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const uint32_t k = (uint32_t)first + (j * 32 + lane) * V + i;
+                    const uint32_t h = mix32(k ^ key);
+                    mc |= encode_m(m[j][i], mi, (h >> 16 << 4) + 8u) << 8 * i;
+                    vc |= encode_v(v[j][i], vi, ((h & 0xFFFFu) << 4) + 8u) << 8 * i;
+                }
+                const int64_t k = at + (j * 32 + lane) * V;
+                *reinterpret_cast<uint32_t*>((uint8_t*)m_ + k) = mc;
+                *reinterpret_cast<uint32_t*>((uint8_t*)v_ + k) = vc;
+            }
+            if (lane == 0) {
+                m_exp[b] = mtop >= 0x7F800000u ? 255 : (uint8_t)(me + 128);
+                v_exp[b] = vtop >= 0x7F800000u ? 255 : (uint8_t)(ve + 128);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int64_t k = at + (j * 32 + lane) * V;
+                Pack<C, V> mp, vp;
+#pragma unroll
+                for (int i = 0; i < V; ++i) mp.v[i] = m[j][i], vp.v[i] = v[j][i];
+                store_pack((C*)m_ + k, mp);
+                store_pack((C*)v_ + k, vp);
+            }
+        }
+    }
+}
+
+// The values that 8-bit states stand for, 4 elements a thread.  Their three
+// fraction bits and exponents fit bfloat16 exactly.
+template <typename O>
+__global__ void __launch_bounds__(256)
+adamw_values_kernel(int64_t quads, const uint32_t* __restrict__ mc,
+                    const uint8_t* __restrict__ me, const uint32_t* __restrict__ vc,
+                    const uint8_t* __restrict__ ve, O* __restrict__ m, O* __restrict__ v) {
+    for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < quads;
+         q += (int64_t)gridDim.x * 256) {
+        const float ms = block_scale(me[q / (kBlock / 4)]), vs = block_scale(ve[q / (kBlock / 4)]);
+        const uint32_t a = mc[q], b = vc[q];
+        Pack<O, 4> x, y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x.v[i] = narrow<O>(decode_m(a >> 8 * i & 0xFFu, ms));
+            y.v[i] = narrow<O>(decode_v(b >> 8 * i & 0xFFu, vs));
+        }
+        store_pack(m + 4 * q, x);
+        store_pack(v + 4 * q, y);
+    }
+}
+
+template <typename P, typename G, bool EIGHT>
+cudaError_t launch(const AdamwTable& tab, const AdamwCall& c, int64_t block0, cudaStream_t s) {
+    using C = typename Compute<P>::type;
+    const double bc1 = 1.0 - std::pow(c.beta1, (double)c.step);
+    const double bc2 = 1.0 - std::pow(c.beta2, (double)c.step);
+    const AdamwScalars<C> a{(C)c.beta1, (C)(1.0 - c.beta1), (C)c.beta2, (C)(1.0 - c.beta2),
+                            (C)(1.0 - c.lr * c.weight_decay), (C)(c.lr / bc1),
+                            (C)(1.0 / std::sqrt(bc2)), (C)c.eps};
+    const size_t each = EIGHT ? 1 : sizeof(C);
+    const int64_t at = block0 * kBlock;
+    const unsigned grid =
+        (unsigned)std::min<int64_t>(((int64_t)tab.blocks + kWarps - 1) / kWarps, 152 * 8);
+    adamw_kernel<P, G, EIGHT><<<grid, 32 * kWarps, 0, s>>>(
+        tab, a, (uint8_t*)c.m + at * each, (uint8_t*)c.v + at * each,
+        EIGHT ? c.m_exp + block0 : nullptr, EIGHT ? c.v_exp + block0 : nullptr,
+        c.copy ? (uint16_t*)c.copy + at : nullptr,
+        !c.copy ? 0 : c.copy_type == CGTP_BF16 ? 1 : 2);
+    count_launch();
+    return cudaGetLastError();
+}
+
+template <typename P, typename G>
+cudaError_t launch_bits(const AdamwTable& tab, const AdamwCall& c, int64_t block0,
+                        cudaStream_t s) {
+    if constexpr (sizeof(P) != 8)
+        if (c.bits == 8) return launch<P, G, true>(tab, c, block0, s);
+    return launch<P, G, false>(tab, c, block0, s);
+}
+
+cudaError_t dispatch(const AdamwTable& tab, const AdamwCall& c, int64_t block0, cudaStream_t s) {
+    if (c.p_type == CGTP_F64) return launch_bits<double, double>(tab, c, block0, s);
+    if (c.p_type == CGTP_BF16)
+        return launch_bits<__nv_bfloat16, __nv_bfloat16>(tab, c, block0, s);
+    if (c.p_type == CGTP_F16) return launch_bits<__half, __half>(tab, c, block0, s);
+    if (c.g_type == CGTP_BF16) return launch_bits<float, __nv_bfloat16>(tab, c, block0, s);
+    if (c.g_type == CGTP_F16) return launch_bits<float, __half>(tab, c, block0, s);
+    return launch_bits<float, float>(tab, c, block0, s);
+}
+
+}  // namespace
+
+cudaError_t launch_adamw(const AdamwCall& c, cudaStream_t s) {
+    const uint32_t seed = mix32(mix32((uint32_t)c.seed) ^ (uint32_t)(c.seed >> 32));
+    const uint32_t key = mix32(seed + (uint32_t)c.step);
+    int64_t block = 0;  // of the flat states
+    for (int i = 0; i < c.n;) {
+        AdamwTable tab;
+        tab.n = 0;
+        const int64_t block0 = block;
+        for (; i < c.n && tab.n < kMaxTensors; ++i) {
+            const int64_t nb = (c.tensors[i].numel + kBlock - 1) / kBlock;
+            if (nb == 0) continue;
+            // block numbers of one launch are 32 bits wide
+            if (tab.n > 0 && block + nb - block0 > 0x7FFFFFFF) break;
+            tab.t[tab.n++] = {c.tensors[i].param, c.tensors[i].grad, c.tensors[i].numel,
+                              (uint32_t)(block - block0), mix32(key + (uint32_t)i)};
+            block += nb;
+        }
+        if (tab.n == 0) continue;
+        tab.blocks = (uint32_t)(block - block0);
+        const cudaError_t e = dispatch(tab, c, block0, s);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_adamw_values(int64_t total, const void* m, const uint8_t* m_exp, const void* v,
+                                const uint8_t* v_exp, cgtp_dtype out_type, void* m_out,
+                                void* v_out, cudaStream_t s) {
+    const int64_t quads = total / 4;
+    const unsigned grid = (unsigned)std::min<int64_t>((quads + 255) / 256, 152 * 32);
+    if (out_type == CGTP_BF16)
+        adamw_values_kernel<<<grid, 256, 0, s>>>(quads, (const uint32_t*)m, m_exp,
+                                                 (const uint32_t*)v, v_exp,
+                                                 (__nv_bfloat16*)m_out, (__nv_bfloat16*)v_out);
+    else
+        adamw_values_kernel<<<grid, 256, 0, s>>>(quads, (const uint32_t*)m, m_exp,
+                                                 (const uint32_t*)v, v_exp, (float*)m_out,
+                                                 (float*)v_out);
+    count_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace cgtp

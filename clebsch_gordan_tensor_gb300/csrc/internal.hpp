@@ -127,6 +127,83 @@ void* tensor_map_encoder();
 cudaError_t launch_radial_w2_tc(int64_t E, int hidden, int64_t n_out, const float* h,
                                 const float* gw, float* partial, int64_t S, cudaStream_t s);
 
+// Per-irrep norm and gated residual (norm_kernels.cuh, norm_<type>.cu).
+constexpr int kNormMaxIrreps = 32;
+constexpr int kNormForwardCtas = 152 * 8, kNormBackwardCtas = 152 * 4;
+struct NormIrrep {
+    int l, mul, off, ch;        // first element of a row, first channel
+    int T, K;                   // threads of a pair, vectors of a thread (0: read again)
+    int cta0, ctas, max_ctas;   // this launch's CTAs; the most, by the irrep's share of a row
+    int64_t part0;              // first element in the gradient's partial rows
+};
+struct NormTable {
+    NormIrrep ir[kNormMaxIrreps];
+    int n = 0, ctas = 0;
+};
+struct NormForward {
+    int64_t n;
+    double eps;
+    cgtp_rows b, x, gate, h, y;
+    const void *weight, *scale, *next_weight;
+};
+struct NormBackward {
+    int64_t n;
+    double eps;
+    cgtp_rows b, h, gate, grad_h, grad_y, grad_x, grad_b, grad_gate;
+    const void *weight, *scale, *next_weight;
+    void *grad_weight, *grad_scale, *grad_next_weight;
+    void* partial;  // NULL: no weight gradients
+    int channels;
+};
+// vectors: every row, weight and multiplicity allows 16-byte accesses (8-byte
+// ones for 16-bit storage).
+#define CGTP_NORM_DECL(t)                                                                  \
+    cudaError_t launch_norm_forward_##t(const NormTable&, const NormForward&, bool vectors, \
+                                        cudaStream_t);                                      \
+    cudaError_t launch_norm_backward_##t(const NormTable&, const NormBackward&, bool vectors, \
+                                         cudaStream_t);
+CGTP_NORM_DECL(f32)
+CGTP_NORM_DECL(f64)
+CGTP_NORM_DECL(bf16)
+CGTP_NORM_DECL(f16)
+#undef CGTP_NORM_DECL
+
+// AdamW over many tensors (adamw.cu).
+constexpr int kAdamwBlock = 256;
+struct AdamwCall {
+    cgtp_dtype p_type, g_type, copy_type;
+    int bits, n;
+    const cgtp_adamw_tensor* tensors;
+    void *m, *v;
+    uint8_t *m_exp, *v_exp;
+    void* copy;  // NULL: none
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;
+    uint64_t seed;
+};
+cudaError_t launch_adamw(const AdamwCall& c, cudaStream_t s);
+cudaError_t launch_adamw_values(int64_t total, const void* m, const uint8_t* m_exp, const void* v,
+                                const uint8_t* v_exp, cgtp_dtype out_type, void* m_out,
+                                void* v_out, cudaStream_t s);
+
+// Embedding lookup and its gradient (embed.cu).
+struct EmbedCall {
+    cgtp_dtype type;
+    int index_bits;
+    int64_t n, v, d;
+    const void* index;
+    double scale;
+    const void* in;   // table [v, d], or gradient rows
+    int64_t in_stride;
+    void* out;        // rows, or the table's gradient [v, d]
+    int64_t out_stride;
+    void* ws;
+};
+cudaError_t launch_embed_forward(const EmbedCall& c, cudaStream_t s);
+size_t embed_backward_workspace_bytes(cgtp_dtype type, int64_t n, int64_t v, int64_t d);
+cudaError_t launch_embed_backward(const EmbedCall& c, cudaStream_t s);
+cudaError_t embed_device_status(int* code);
+
 // Partial weight-gradient rows a shared-weight backward may write (grid cap).
 constexpr int64_t kSharedWRows = 2048;
 

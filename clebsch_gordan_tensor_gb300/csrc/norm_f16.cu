@@ -1,0 +1,15 @@
+// The per-irrep norm and gated residual on rows stored as f16.
+#include "norm_kernels.cuh"
+
+namespace cgtp {
+
+cudaError_t launch_norm_forward_f16(const NormTable& tab, const NormForward& a, bool vectors,
+                                   cudaStream_t s) {
+    return forward<__half>(tab, a, vectors, s);
+}
+cudaError_t launch_norm_backward_f16(const NormTable& tab, const NormBackward& a, bool vectors,
+                                    cudaStream_t s) {
+    return backward<__half>(tab, a, vectors, s);
+}
+
+}  // namespace cgtp

@@ -1,0 +1,15 @@
+// The per-irrep norm and gated residual on rows stored as f64.
+#include "norm_kernels.cuh"
+
+namespace cgtp {
+
+cudaError_t launch_norm_forward_f64(const NormTable& tab, const NormForward& a, bool vectors,
+                                   cudaStream_t s) {
+    return forward<double>(tab, a, vectors, s);
+}
+cudaError_t launch_norm_backward_f64(const NormTable& tab, const NormBackward& a, bool vectors,
+                                    cudaStream_t s) {
+    return backward<double>(tab, a, vectors, s);
+}
+
+}  // namespace cgtp

@@ -1,0 +1,427 @@
+// C-ABI entry points of the training operators: the embedding and its
+// gradient, the per-irrep norm and gated residual, AdamW.  Every call checks
+// its arguments on the host and launches on the caller's stream; none
+// allocates device memory.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <initializer_list>
+#include <memory>
+#include <new>
+#include <string>
+#include <vector>
+
+#include "cgtp.h"
+#include "internal.hpp"
+
+struct cgtp_norm_s {
+    cgtp_dtype dtype = CGTP_F32;
+    double eps = 0;
+    int64_t dim = 0, channels = 0, partial = 0;  // partial: values of all CTAs' rows
+    cgtp::NormTable forward, backward;           // with each direction's CTA shares
+};
+
+namespace cgtp {
+
+static cgtp_status tfail(cgtp_status s, const std::string& m) {
+    set_error_message(m);
+    return s;
+}
+
+static cgtp_status tcuda(cudaError_t e, const char* what) {
+    if (e == cudaSuccess) return CGTP_OK;
+    set_cuda_error(e);
+    return tfail(CGTP_E_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+}
+
+static bool known(cgtp_dtype t) {
+    return t == CGTP_F32 || t == CGTP_F64 || t == CGTP_BF16 || t == CGTP_F16;
+}
+static size_t size_of(cgtp_dtype t) { return t == CGTP_F64 ? 8 : t == CGTP_F32 ? 4 : 2; }
+static bool on(const void* p, size_t a) { return (uintptr_t)p % a == 0; }
+
+static cgtp_status embed_check(cgtp_dtype dtype, int index_bits, int64_t N, int64_t V, int64_t D,
+                               int64_t stride, int64_t least) {
+    if (!known(dtype)) return tfail(CGTP_E_ARG, "bad dtype");
+    if (index_bits != 32 && index_bits != 64)
+        return tfail(CGTP_E_ARG, "index_bits must be 32 or 64");
+    if (N < 0 || V < 0 || N >= ((int64_t)1 << 31) || V >= ((int64_t)1 << 31) - 1 || D < 1)
+        return tfail(CGTP_E_ARG, "sizes out of range: 0 <= N, V < 2^31, D >= 1");
+    if (D > ((int64_t)1 << 31)) return tfail(CGTP_E_ARG, "row width out of range");
+    if (stride < least && N > 1) return tfail(CGTP_E_ARG, "row stride out of range");
+    if (stride > ((int64_t)1 << 40) / std::max<int64_t>(1, N))
+        return tfail(CGTP_E_ARG, "row stride too large");
+    return CGTP_OK;
+}
+
+static bool irrep_tables(cgtp_norm_s& h, const std::vector<Irrep>& irreps) {
+    int64_t off = 0, ch = 0;
+    for (auto& ir : irreps) {
+        off += (int64_t)ir.mul * (2 * ir.l + 1);
+        ch += ir.mul;
+    }
+    if (off >= ((int64_t)1 << 30)) return false;
+    h.dim = off;
+    h.channels = ch;
+    off = ch = 0;
+    int64_t part = 0;
+    for (size_t i = 0; i < irreps.size(); ++i) {
+        const Irrep& ir = irreps[i];
+        const int64_t width = (int64_t)ir.mul * (2 * ir.l + 1);
+        NormIrrep e{};
+        e.l = ir.l;
+        e.mul = ir.mul;
+        e.off = (int)off;
+        e.ch = (int)ch;
+        // a share of the CTAs by the share of the row
+        e.max_ctas = (int)std::max<int64_t>(1, kNormForwardCtas * width / h.dim);
+        h.forward.ir[i] = e;
+        e.max_ctas = (int)std::max<int64_t>(1, kNormBackwardCtas * width / h.dim);
+        e.part0 = part;
+        part += (int64_t)e.max_ctas * 3 * ir.mul;
+        h.backward.ir[i] = e;
+        off += width;
+        ch += ir.mul;
+    }
+    h.forward.n = h.backward.n = (int)irreps.size();
+    h.partial = part;
+    return true;
+}
+
+static size_t norm_ws(const cgtp_norm_s& h) {
+    return (size_t)h.partial * (h.dtype == CGTP_F64 ? 8 : 4);
+}
+
+// Rows of `width` elements: the address and, for outputs, that rows lie apart.
+static cgtp_status rows_check(const cgtp_norm_s& h, int64_t n, const cgtp_rows& r, int64_t width,
+                              bool out, const char* name) {
+    if (!r.data) return CGTP_OK;
+    if (!on(r.data, size_of(h.dtype)))
+        return tfail(CGTP_E_ARG, std::string(name) + " is not aligned to its element");
+    if (n > 1 && (r.stride < 0 || r.stride > ((int64_t)1 << 40) / n))
+        return tfail(CGTP_E_ARG, std::string(name) + " has a stride out of range");
+    if (out && n > 1 && r.stride < width)
+        return tfail(CGTP_E_ARG, std::string(name) + " has rows that overlap");
+    return CGTP_OK;
+}
+
+static cgtp_status norm_check(cgtp_norm h, int64_t n, std::initializer_list<const void*> params) {
+    if (!h) return tfail(CGTP_E_ARG, "NULL norm");
+    if (n < 0 || n > ((int64_t)1 << 40) / h->dim) return tfail(CGTP_E_ARG, "row count out of range");
+    for (const void* p : params)
+        if (!on(p, h->dtype == CGTP_F64 ? 8 : 4))
+            return tfail(CGTP_E_ARG, "weight pointer not aligned to its element");
+    return CGTP_OK;
+}
+
+// 16-byte accesses (8-byte ones for 16-bit rows) everywhere.
+static bool norm_vectors(const cgtp_norm_s& h, std::initializer_list<cgtp_rows> rows) {
+    const int V = h.dtype == CGTP_F64 ? 2 : 4;
+    for (int i = 0; i < h.forward.n; ++i)
+        if (h.forward.ir[i].mul % V) return false;
+    for (const cgtp_rows& r : rows)
+        if (r.data && (!on(r.data, V * size_of(h.dtype)) || r.stride % V)) return false;
+    return true;
+}
+
+static cudaError_t run_forward(const cgtp_norm_s& h, const NormForward& a, cudaStream_t s) {
+    const bool v = norm_vectors(h, {a.b, a.x, a.gate, a.h, a.y});
+    switch (h.dtype) {
+        case CGTP_F64: return launch_norm_forward_f64(h.forward, a, v, s);
+        case CGTP_BF16: return launch_norm_forward_bf16(h.forward, a, v, s);
+        case CGTP_F16: return launch_norm_forward_f16(h.forward, a, v, s);
+        default: return launch_norm_forward_f32(h.forward, a, v, s);
+    }
+}
+
+static cudaError_t run_backward(const cgtp_norm_s& h, const NormBackward& a, cudaStream_t s) {
+    const bool v = norm_vectors(
+        h, {a.b, a.h, a.gate, a.grad_h, a.grad_y, a.grad_x, a.grad_b, a.grad_gate});
+    switch (h.dtype) {
+        case CGTP_F64: return launch_norm_backward_f64(h.backward, a, v, s);
+        case CGTP_BF16: return launch_norm_backward_bf16(h.backward, a, v, s);
+        case CGTP_F16: return launch_norm_backward_f16(h.backward, a, v, s);
+        default: return launch_norm_backward_f32(h.backward, a, v, s);
+    }
+}
+
+static cgtp_status zero_params(const cgtp_norm_s& h, std::initializer_list<void*> outs,
+                               cudaStream_t s) {
+    for (void* p : outs)
+        if (p) {
+            cgtp_status st = tcuda(
+                launch_fill_zero(p, h.channels * (h.dtype == CGTP_F64 ? 8 : 4), s), "zero fill");
+            if (st != CGTP_OK) return st;
+        }
+    return CGTP_OK;
+}
+
+}  // namespace cgtp
+
+using namespace cgtp;
+
+#define GUARD_BEGIN try {
+#define GUARD_END                                                  \
+    }                                                              \
+    catch (const std::bad_alloc&) {                                \
+        return tfail(CGTP_E_NOMEM, "host allocation failed");      \
+    }                                                              \
+    catch (...) {                                                  \
+        return tfail(CGTP_E_ARG, "unexpected internal exception"); \
+    }
+
+static inline cudaStream_t S(cgtp_stream s) { return reinterpret_cast<cudaStream_t>(s); }
+
+extern "C" {
+
+// ------------------------------------------------------------- embedding --
+
+cgtp_status cgtp_embed_forward(cgtp_dtype dtype, int index_bits, int64_t N, int64_t V, int64_t D,
+                               const void* index, const void* table, double scale, void* out,
+                               int64_t out_stride, cgtp_stream stream) {
+    GUARD_BEGIN
+    cgtp_status st = embed_check(dtype, index_bits, N, V, D, out_stride, D);
+    if (st != CGTP_OK || N == 0) return st;
+    if (!index || (!table && V > 0) || !out) return tfail(CGTP_E_ARG, "NULL tensor");
+    if (!on(index, index_bits / 8) || !on(table, size_of(dtype)) || !on(out, size_of(dtype)))
+        return tfail(CGTP_E_ARG, "tensor pointer not aligned to its element");
+    const EmbedCall c{dtype, index_bits, N, V, D, index, scale, table, D, out, out_stride, nullptr};
+    return tcuda(launch_embed_forward(c, S(stream)), "embed_forward");
+    GUARD_END
+}
+
+cgtp_status cgtp_embed_backward_workspace(cgtp_dtype dtype, int64_t N, int64_t V, int64_t D,
+                                          size_t* bytes) {
+    GUARD_BEGIN
+    cgtp_status st = embed_check(dtype, 32, N, V, D, D, D);
+    if (st != CGTP_OK) return st;
+    if (!bytes) return tfail(CGTP_E_ARG, "NULL output");
+    *bytes = embed_backward_workspace_bytes(dtype, N, V, D);
+    return CGTP_OK;
+    GUARD_END
+}
+
+cgtp_status cgtp_embed_backward(cgtp_dtype dtype, int index_bits, int64_t N, int64_t V, int64_t D,
+                                const void* index, const void* grad_out, int64_t grad_stride,
+                                double scale, void* grad_table, void* workspace,
+                                size_t workspace_bytes, cgtp_stream stream) {
+    GUARD_BEGIN
+    cgtp_status st = embed_check(dtype, index_bits, N, V, D, grad_stride, 0);
+    if (st != CGTP_OK || V == 0) return st;
+    if (!grad_table || (N > 0 && (!index || !grad_out))) return tfail(CGTP_E_ARG, "NULL tensor");
+    if (!on(index, index_bits / 8) || !on(grad_out, size_of(dtype)) ||
+        !on(grad_table, size_of(dtype)))
+        return tfail(CGTP_E_ARG, "tensor pointer not aligned to its element");
+    const size_t need = embed_backward_workspace_bytes(dtype, N, V, D);
+    if (need && (!workspace || !on(workspace, 256) || workspace_bytes < need))
+        return tfail(CGTP_E_ARG, "the embedding gradient needs a 256-byte aligned workspace of "
+                                 "cgtp_embed_backward_workspace() bytes");
+    const EmbedCall c{dtype, index_bits, N,    V,          D, index,
+                      scale, grad_out,   grad_stride, grad_table, D, workspace};
+    return tcuda(launch_embed_backward(c, S(stream)), "embed_backward");
+    GUARD_END
+}
+
+cgtp_status cgtp_embed_device_status(int* code) {
+    GUARD_BEGIN
+    if (!code) return tfail(CGTP_E_ARG, "NULL output");
+    return tcuda(embed_device_status(code), "embed_device_status");
+    GUARD_END
+}
+
+// ------------------------------------------------ norm and gated residual --
+
+cgtp_status cgtp_norm_create(cgtp_norm* out, const char* irreps, double eps, cgtp_dtype dtype) {
+    GUARD_BEGIN
+    if (!out) return tfail(CGTP_E_ARG, "NULL output handle");
+    *out = nullptr;
+    if (!known(dtype)) return tfail(CGTP_E_ARG, "bad dtype");
+    if (!(eps > 0) || !std::isfinite(eps)) return tfail(CGTP_E_ARG, "eps must be positive");
+    std::vector<Irrep> parsed;
+    std::string err;
+    if (!parse_irreps(irreps, parsed, err)) return tfail(CGTP_E_IRREPS, err);
+    if ((int)parsed.size() > kNormMaxIrreps)
+        return tfail(CGTP_E_UNSUPPORTED, "more than 32 irreps in one row");
+    auto h = std::make_unique<cgtp_norm_s>();
+    h->dtype = dtype;
+    h->eps = eps;
+    if (!irrep_tables(*h, parsed)) return tfail(CGTP_E_UNSUPPORTED, "row too wide");
+    *out = h.release();
+    return CGTP_OK;
+    GUARD_END
+}
+
+cgtp_status cgtp_norm_destroy(cgtp_norm norm) {
+    delete norm;
+    return CGTP_OK;
+}
+
+cgtp_status cgtp_norm_info(cgtp_norm norm, int64_t* dim, int64_t* channels) {
+    GUARD_BEGIN
+    if (!norm) return tfail(CGTP_E_ARG, "NULL norm");
+    if (dim) *dim = norm->dim;
+    if (channels) *channels = norm->channels;
+    return CGTP_OK;
+    GUARD_END
+}
+
+cgtp_status cgtp_norm_workspace(cgtp_norm norm, size_t* bytes) {
+    GUARD_BEGIN
+    if (!norm || !bytes) return tfail(CGTP_E_ARG, "NULL argument");
+    *bytes = norm_ws(*norm);
+    return CGTP_OK;
+    GUARD_END
+}
+
+cgtp_status cgtp_residual_forward(cgtp_norm norm, int64_t n, cgtp_rows x, cgtp_rows b,
+                                  const void* weight, cgtp_rows gate, const void* scale,
+                                  const void* next_weight, cgtp_rows h, cgtp_rows y,
+                                  cgtp_stream stream) {
+    GUARD_BEGIN
+    cgtp_status st = norm_check(norm, n, {weight, scale, next_weight});
+    if (st != CGTP_OK || n == 0) return st;
+    if (!b.data || !h.data) return tfail(CGTP_E_ARG, "NULL tensor");
+    if (y.data == h.data) return tfail(CGTP_E_ARG, "y may not be h");
+    if ((st = rows_check(*norm, n, x, norm->dim, false, "x")) != CGTP_OK ||
+        (st = rows_check(*norm, n, b, norm->dim, false, "b")) != CGTP_OK ||
+        (st = rows_check(*norm, n, gate, norm->channels, false, "gate")) != CGTP_OK ||
+        (st = rows_check(*norm, n, h, norm->dim, true, "h")) != CGTP_OK ||
+        (st = rows_check(*norm, n, y, norm->dim, true, "y")) != CGTP_OK)
+        return st;
+    const NormForward a{n, norm->eps, b, x, gate, h, y, weight, scale, next_weight};
+    return tcuda(run_forward(*norm, a, S(stream)), "residual_forward");
+    GUARD_END
+}
+
+cgtp_status cgtp_norm_forward(cgtp_norm norm, int64_t n, cgtp_rows x, const void* weight,
+                              cgtp_rows y, cgtp_stream stream) {
+    const cgtp_rows none{nullptr, 0};
+    return cgtp_residual_forward(norm, n, none, x, weight, none, nullptr, nullptr, y, none, stream);
+}
+
+cgtp_status cgtp_residual_backward(cgtp_norm norm, int64_t n, cgtp_rows b, cgtp_rows h,
+                                   const void* weight, cgtp_rows gate, const void* scale,
+                                   const void* next_weight, cgtp_rows grad_h, cgtp_rows grad_y,
+                                   cgtp_rows grad_x, cgtp_rows grad_b, cgtp_rows grad_gate,
+                                   void* grad_weight, void* grad_scale, void* grad_next_weight,
+                                   void* workspace, size_t workspace_bytes, cgtp_stream stream) {
+    GUARD_BEGIN
+    cgtp_status st = norm_check(
+        norm, n, {weight, scale, next_weight, grad_weight, grad_scale, grad_next_weight});
+    if (st != CGTP_OK) return st;
+    if (n == 0)
+        return zero_params(*norm, {grad_weight, grad_scale, grad_next_weight}, S(stream));
+    if (!b.data || (!grad_h.data && !grad_y.data) || (grad_y.data && !h.data))
+        return tfail(CGTP_E_ARG, "NULL tensor");
+    if ((st = rows_check(*norm, n, b, norm->dim, false, "b")) != CGTP_OK ||
+        (st = rows_check(*norm, n, h, norm->dim, false, "h")) != CGTP_OK ||
+        (st = rows_check(*norm, n, gate, norm->channels, false, "gate")) != CGTP_OK ||
+        (st = rows_check(*norm, n, grad_h, norm->dim, false, "grad_h")) != CGTP_OK ||
+        (st = rows_check(*norm, n, grad_y, norm->dim, false, "grad_y")) != CGTP_OK ||
+        (st = rows_check(*norm, n, grad_x, norm->dim, true, "grad_x")) != CGTP_OK ||
+        (st = rows_check(*norm, n, grad_b, norm->dim, true, "grad_b")) != CGTP_OK ||
+        (st = rows_check(*norm, n, grad_gate, norm->channels, true, "grad_gate")) != CGTP_OK)
+        return st;
+    for (const void* in : {b.data, h.data, gate.data, grad_h.data, grad_y.data})
+        for (const void* o : {grad_x.data, grad_b.data, grad_gate.data})
+            if (o && in == o) return tfail(CGTP_E_ARG, "an output is one of the inputs");
+    const bool sums = grad_weight || grad_scale || grad_next_weight;
+    if (sums && (!workspace || !on(workspace, 256) || workspace_bytes < norm_ws(*norm)))
+        return tfail(CGTP_E_ARG, "the weight gradients need a 256-byte aligned workspace of "
+                                 "cgtp_norm_workspace() bytes");
+    const NormBackward a{n,      norm->eps, b,           h,          gate,
+                         grad_h, grad_y,    grad_x,      grad_b,     grad_gate,
+                         weight, scale,     next_weight, grad_weight, grad_scale,
+                         grad_next_weight, sums ? workspace : nullptr, (int)norm->channels};
+    return tcuda(run_backward(*norm, a, S(stream)), "residual_backward");
+    GUARD_END
+}
+
+cgtp_status cgtp_norm_backward(cgtp_norm norm, int64_t n, cgtp_rows x, const void* weight,
+                               cgtp_rows grad_y, cgtp_rows grad_x, void* grad_weight,
+                               void* workspace, size_t workspace_bytes, cgtp_stream stream) {
+    const cgtp_rows none{nullptr, 0};
+    return cgtp_residual_backward(norm, n, x, none, weight, none, nullptr, nullptr, grad_y, none,
+                                  none, grad_x, none, grad_weight, nullptr, nullptr, workspace,
+                                  workspace_bytes, stream);
+}
+
+// ----------------------------------------------------------------- AdamW --
+
+cgtp_status cgtp_adamw_layout(int n, const int64_t* numel, int64_t* first, int64_t* total) {
+    GUARD_BEGIN
+    if (n < 0 || (n > 0 && !numel) || !total) return tfail(CGTP_E_ARG, "NULL argument");
+    int64_t at = 0;
+    for (int i = 0; i < n; ++i) {
+        if (numel[i] < 0 || numel[i] > ((int64_t)1 << 38))
+            return tfail(CGTP_E_ARG, "tensor length out of range");
+        if (first) first[i] = at;
+        at += (numel[i] + kAdamwBlock - 1) / kAdamwBlock * kAdamwBlock;
+    }
+    *total = at;
+    return CGTP_OK;
+    GUARD_END
+}
+
+cgtp_status cgtp_adamw_step(cgtp_dtype param_dtype, cgtp_dtype grad_dtype, int state_bits, int n,
+                            const cgtp_adamw_tensor* tensors, void* m, void* v, uint8_t* m_exp,
+                            uint8_t* v_exp, void* copy, cgtp_dtype copy_dtype,
+                            const cgtp_adamw_args* args, cgtp_stream stream) {
+    GUARD_BEGIN
+    if (!known(param_dtype) || !known(grad_dtype)) return tfail(CGTP_E_ARG, "bad dtype");
+    if (state_bits != 8 && state_bits != 32)
+        return tfail(CGTP_E_ARG, "state_bits must be 8 or 32");
+    if (param_dtype != grad_dtype && (param_dtype != CGTP_F32 || grad_dtype == CGTP_F64))
+        return tfail(CGTP_E_UNSUPPORTED, "gradients of another type: fp32 parameters with 16-bit "
+                                         "gradients only");
+    if (param_dtype == CGTP_F64 && (state_bits == 8 || copy))
+        return tfail(CGTP_E_UNSUPPORTED, "fp64 parameters keep 64-bit states and no copies");
+    if (copy && copy_dtype != CGTP_BF16 && copy_dtype != CGTP_F16)
+        return tfail(CGTP_E_ARG, "copies are bfloat16 or binary16");
+    if (n < 0 || (n > 0 && !tensors) || !args) return tfail(CGTP_E_ARG, "NULL argument");
+    if (!(args->eps > 0) || !(args->beta1 >= 0 && args->beta1 < 1) ||
+        !(args->beta2 >= 0 && args->beta2 < 1) || args->step < 1 || !std::isfinite(args->lr) ||
+        !std::isfinite(args->weight_decay))
+        return tfail(CGTP_E_ARG, "need eps > 0, 0 <= beta < 1, step >= 1, finite lr and "
+                                 "weight_decay");
+    bool any = false;
+    for (int i = 0; i < n; ++i) {
+        const cgtp_adamw_tensor& t = tensors[i];
+        if (t.numel < 0 || t.numel > ((int64_t)1 << 38))
+            return tfail(CGTP_E_ARG, "tensor length out of range");
+        if (t.numel == 0) continue;
+        any = true;
+        if (!t.param || !t.grad) return tfail(CGTP_E_ARG, "NULL tensor");
+        if (!on(t.param, size_of(param_dtype)) || !on(t.grad, size_of(grad_dtype)))
+            return tfail(CGTP_E_ARG, "tensor pointer not aligned to its element");
+    }
+    if (!any) return CGTP_OK;
+    if (!m || !v || (state_bits == 8 && (!m_exp || !v_exp)))
+        return tfail(CGTP_E_ARG, "NULL state");
+    if (!on(m, 256) || !on(v, 256) || !on(copy, 256))
+        return tfail(CGTP_E_ARG, "flat arrays must be 256-byte aligned");
+    const AdamwCall c{param_dtype, grad_dtype, copy_dtype, state_bits, n, tensors, m, v, m_exp,
+                      v_exp, copy, args->lr, args->beta1, args->beta2, args->eps,
+                      args->weight_decay, args->step, args->seed};
+    return tcuda(launch_adamw(c, S(stream)), "adamw_step");
+    GUARD_END
+}
+
+cgtp_status cgtp_adamw_values(int64_t total, const void* m, const uint8_t* m_exp, const void* v,
+                              const uint8_t* v_exp, cgtp_dtype out_dtype, void* m_out, void* v_out,
+                              cgtp_stream stream) {
+    GUARD_BEGIN
+    if (total < 0 || total % kAdamwBlock) return tfail(CGTP_E_ARG, "bad length");
+    if (out_dtype != CGTP_F32 && out_dtype != CGTP_BF16)
+        return tfail(CGTP_E_ARG, "values are fp32 or bfloat16");
+    if (total == 0) return CGTP_OK;
+    if (!m || !v || !m_exp || !v_exp || !m_out || !v_out) return tfail(CGTP_E_ARG, "NULL tensor");
+    if (!on(m, 256) || !on(v, 256) || !on(m_out, 256) || !on(v_out, 256))
+        return tfail(CGTP_E_ARG, "flat arrays must be 256-byte aligned");
+    return tcuda(launch_adamw_values(total, m, m_exp, v, v_exp, out_dtype, m_out, v_out, S(stream)),
+                 "adamw_values");
+    GUARD_END
+}
+
+}  // extern "C"

@@ -1,0 +1,300 @@
+"""The trainable frame around the tensor product: the embedding that makes the
+first node features, the per-irrep norm and gated residual around a block, and
+the AdamW step over a network's parameters.
+
+As in the rest of the binding, this marshals torch CUDA tensors into the C ABI
+and the current torch stream; the computation runs in the library's kernels.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import (BF16, F16, F32, F64, CgtpError, _AdamwArgs, _AdamwTensor, _check, _need, _ptr,
+               _Rows, _stream, lib)
+
+_TYPES = {torch.float32: F32, torch.float64: F64, torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _type(dtype) -> int:
+    if dtype not in _TYPES:
+        raise CgtpError(f"unsupported dtype {dtype}")
+    return _TYPES[dtype]
+
+
+def _rows(t, name, dtype, shape):
+    """Rows of a tensor, which may lie further apart than they are wide."""
+    if t is None:
+        return _Rows(None, 0)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise CgtpError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise CgtpError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise CgtpError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(1) != 1 and shape[1] != 1:
+        raise CgtpError(f"{name} must have contiguous rows")
+    return _Rows(t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1])
+
+
+def _scratch(nbytes, device):
+    return torch.empty(max(256, nbytes), dtype=torch.uint8, device=device)
+
+
+# ------------------------------------------------------------- embedding --
+
+def _index(index):
+    if not isinstance(index, torch.Tensor) or not index.is_cuda:
+        raise CgtpError("index must be a CUDA tensor")
+    if index.dtype not in (torch.int32, torch.int64) or index.dim() != 1:
+        raise CgtpError(f"index must be a row of int32 or int64, got {index.dtype} of "
+                        f"{index.dim()} dimensions")
+    if not index.is_contiguous():
+        raise CgtpError("index must be contiguous")
+    return index.element_size() * 8
+
+
+def embed_forward(index, table, scale: float = 1.0, out=None):
+    """out[n] = scale * table[index[n]].  index [N] int32 or int64 (negative:
+    padding, a zero row); table [V, D] fp32, fp64, bfloat16 or binary16.  ``out``
+    [N, D] may be a block of wider rows, such as the scalar channels of a
+    feature row; the rest of those rows is left as it is."""
+    bits = _index(index)
+    _need(table, "table", table.dtype)
+    if table.dim() != 2:
+        raise CgtpError(f"table has {table.dim()} dimensions, expected 2")
+    n, (v, d) = index.shape[0], table.shape
+    if out is None:
+        out = torch.empty(n, d, dtype=table.dtype, device=table.device)
+    o = _rows(out, "out", table.dtype, (n, d))
+    _check(lib().cgtp_embed_forward(_type(table.dtype), bits, n, v, d, _ptr(index), _ptr(table),
+                                    float(scale), o.data, o.stride, _stream()))
+    return out
+
+
+def embed_backward(index, grad_out, n_rows: int, scale: float = 1.0, out=None, workspace=None):
+    """The gradient of embed_forward's table [n_rows, D]: scale times the sum of
+    the rows of grad_out [N, D] at each index, zero rows where there is none.
+    Deterministic."""
+    bits = _index(index)
+    n = index.shape[0]
+    if not isinstance(grad_out, torch.Tensor) or grad_out.dim() != 2:
+        raise CgtpError("grad_out must be a tensor of rows")
+    d = grad_out.shape[1]
+    g = _rows(grad_out, "grad_out", grad_out.dtype, (n, d))
+    if out is None:
+        out = torch.empty(n_rows, d, dtype=grad_out.dtype, device=grad_out.device)
+    _need(out, "out", grad_out.dtype, (n_rows, d))
+    ty = _type(grad_out.dtype)
+    if workspace is None:
+        nb = ctypes.c_size_t()
+        _check(lib().cgtp_embed_backward_workspace(ty, n, n_rows, d, ctypes.byref(nb)))
+        workspace = _scratch(nb.value, grad_out.device)
+    _check(lib().cgtp_embed_backward(ty, bits, n, n_rows, d, _ptr(index), g.data, g.stride,
+                                     float(scale), _ptr(out), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(), _stream()))
+    return out
+
+
+def embed_device_status() -> int:
+    """1 if an index past the table was met since the last query, then cleared
+    (synchronous)."""
+    c = ctypes.c_int()
+    _check(lib().cgtp_embed_device_status(ctypes.byref(c)))
+    return c.value
+
+
+# ---------------------------------------------- norms and gated residuals --
+
+class IrrepsNorm:
+    """Equivariant RMS norm of feature rows (``irreps``), alone and fused with
+    the gate, the residual scale and the next norm after a block:
+
+        norm(b) = b * weight / sqrt(mean over the irrep of b^2 + eps)
+        h = x + scale * sigmoid(gate) * norm(b)
+        y = norm(h) with next_weight
+
+    ``weight``, ``scale``, ``next_weight`` [channels] hold one value per irrep
+    and channel (fp32; fp64 for fp64 rows), ``gate`` [n, channels] one per row
+    too; ``None`` is 1.  Rows are stored in ``dtype`` (fp32, fp64, bfloat16,
+    binary16) and may lie further apart than they are wide.  "Dx0e" is the plain
+    RMS norm of rows of D."""
+
+    def __init__(self, irreps: str, eps: float = 1e-5, dtype=torch.float32):
+        self.irreps, self.eps, self.dtype = irreps, float(eps), dtype
+        self.wdtype = torch.float64 if dtype == torch.float64 else torch.float32
+        h = ctypes.c_void_p()
+        _check(lib().cgtp_norm_create(ctypes.byref(h), irreps.encode(), self.eps, _type(dtype)))
+        self._h = h
+        a, b, c = ctypes.c_int64(), ctypes.c_int64(), ctypes.c_size_t()
+        _check(lib().cgtp_norm_info(h, ctypes.byref(a), ctypes.byref(b)))
+        _check(lib().cgtp_norm_workspace(h, ctypes.byref(c)))
+        self.dim, self.channels, self.workspace_bytes = a.value, b.value, c.value
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None:
+            lib().cgtp_norm_destroy(h)
+            self._h = None
+
+    def _w(self, t, name):
+        _need(t, name, self.wdtype, (self.channels,))
+        return _ptr(t)
+
+    def _in(self, t, name, n, width=None):
+        return _rows(t, name, self.dtype, (n, self.dim if width is None else width))
+
+    def _new(self, like, width=None):
+        return torch.empty(like.shape[0], self.dim if width is None else width, dtype=self.dtype,
+                           device=like.device)
+
+    def _new_w(self, like, need):
+        return torch.empty(self.channels, dtype=self.wdtype, device=like.device) if need else None
+
+    def forward(self, x, weight=None, out=None):
+        """y = norm(x)."""
+        n = x.shape[0]
+        xr = self._in(x, "x", n)
+        if out is None:
+            out = self._new(x)
+        _check(lib().cgtp_norm_forward(self._h, n, xr, self._w(weight, "weight"),
+                                       self._in(out, "out", n), _stream()))
+        return out
+
+    def backward(self, x, grad_out, weight=None, need=(True, True), workspace=None):
+        """(grad_x, grad_weight); an entry is None where ``need`` is False."""
+        n = x.shape[0]
+        xr, gr = self._in(x, "x", n), self._in(grad_out, "grad_out", n)
+        gx = self._new(x) if need[0] else None
+        gw = self._new_w(x, need[1])
+        if gw is not None and workspace is None:
+            workspace = _scratch(self.workspace_bytes, x.device)
+        _check(lib().cgtp_norm_backward(
+            self._h, n, xr, self._w(weight, "weight"), gr, self._in(gx, "grad_x", n), _ptr(gw),
+            _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream()))
+        return gx, gw
+
+    def residual_forward(self, x, b, weight=None, gate=None, scale=None, next_weight=None,
+                         norm_next: bool = True, out=None):
+        """(h, y): the residual stream after a block with output ``b`` and, unless
+        ``norm_next`` is False (then None), its norm.  ``out``: (h, y) to write;
+        h may be x or b."""
+        n = b.shape[0]
+        h, y = out if out is not None else (self._new(b), self._new(b) if norm_next else None)
+        _check(lib().cgtp_residual_forward(
+            self._h, n, self._in(x, "x", n), self._in(b, "b", n), self._w(weight, "weight"),
+            self._in(gate, "gate", n, self.channels), self._w(scale, "scale"),
+            self._w(next_weight, "next_weight"), self._in(h, "h", n), self._in(y, "y", n),
+            _stream()))
+        return h, y
+
+    def residual_backward(self, b, h, grad_h, grad_y=None, weight=None, gate=None, scale=None,
+                          next_weight=None, need=(True,) * 6, workspace=None):
+        """(grad_x, grad_b, grad_gate, grad_weight, grad_scale, grad_next_weight)
+        for the cotangents of residual_forward's h and y (either may be None);
+        ``h`` as it returned it (None without grad_y).  Entries not in ``need``
+        and those of absent arguments (gate) are None."""
+        n = b.shape[0]
+        rows = [self._in(t, name, n) for t, name in
+                ((b, "b"), (h, "h"), (grad_h, "grad_h"), (grad_y, "grad_y"))]
+        gx = self._new(b) if need[0] else None
+        gb = self._new(b) if need[1] else None
+        gz = self._new(b, self.channels) if need[2] and gate is not None else None
+        gw, gs = self._new_w(b, need[3]), self._new_w(b, need[4])
+        gn = self._new_w(b, need[5] and grad_y is not None)
+        if (gw is not None or gs is not None or gn is not None) and workspace is None:
+            workspace = _scratch(self.workspace_bytes, b.device)
+        _check(lib().cgtp_residual_backward(
+            self._h, n, rows[0], rows[1], self._w(weight, "weight"),
+            self._in(gate, "gate", n, self.channels), self._w(scale, "scale"),
+            self._w(next_weight, "next_weight"), rows[2], rows[3], self._in(gx, "grad_x", n),
+            self._in(gb, "grad_b", n), self._in(gz, "grad_gate", n, self.channels), _ptr(gw),
+            _ptr(gs), _ptr(gn), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+            _stream()))
+        return gx, gb, gz, gw, gs, gn
+
+
+# ----------------------------------------------------------------- AdamW --
+
+class AdamW:
+    """AdamW over a list of parameter tensors, updated in place, one launch per
+    64 tensors.  Parameters of one dtype: fp32 (gradients fp32, bfloat16 or
+    binary16), fp64, bfloat16 or binary16.
+
+    ``state_bits=8`` holds the moments in one byte each (``m``, ``v``) with one
+    exponent byte per 256 elements (``m_exp``, ``v_exp``), rounded
+    stochastically from ``seed``; ``state_values()`` gives what they stand for.
+    ``copy_dtype`` keeps the parameters' 16-bit copies in ``copies`` (one tensor
+    per parameter, for plans with 16-bit weights).  ``m``, ``v``, ``copy`` are
+    flat: parameter i's elements start at ``first[i]``.  ``step_count`` is the
+    number of steps taken; it and the state tensors are all there is to save."""
+
+    def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay: float = 0.01, state_bits: int = 32, copy_dtype=None, seed: int = 0):
+        self.params = list(params)
+        if not self.params:
+            raise CgtpError("no parameters")
+        self.dtype, self.device = self.params[0].dtype, self.params[0].device
+        for i, p in enumerate(self.params):
+            _need(p, f"parameter {i}", self.dtype)
+        _type(self.dtype)
+        if state_bits not in (8, 32) or (state_bits == 8 and self.dtype == torch.float64):
+            raise CgtpError(f"state_bits {state_bits} is not supported for {self.dtype}")
+        if copy_dtype not in (None, torch.bfloat16, torch.float16) or (
+                copy_dtype is not None and self.dtype == torch.float64):
+            raise CgtpError(f"copy_dtype {copy_dtype} is not supported for {self.dtype}")
+        self.lr, self.betas, self.eps = float(lr), (float(betas[0]), float(betas[1])), float(eps)
+        self.weight_decay, self.state_bits, self.seed = float(weight_decay), state_bits, int(seed)
+        self.step_count = 0
+        n = len(self.params)
+        numel = (ctypes.c_int64 * n)(*[p.numel() for p in self.params])
+        first, total = (ctypes.c_int64 * n)(), ctypes.c_int64()
+        _check(lib().cgtp_adamw_layout(n, numel, first, ctypes.byref(total)))
+        self.first, self.total = list(first), total.value
+        state = torch.uint8 if state_bits == 8 else (
+            torch.float64 if self.dtype == torch.float64 else torch.float32)
+        zeros = lambda k, t: torch.zeros(max(k, 1), dtype=t, device=self.device)[:k]  # noqa: E731
+        self.m, self.v = zeros(self.total, state), zeros(self.total, state)
+        self.m_exp = self.v_exp = None
+        if state_bits == 8:
+            self.m_exp, self.v_exp = (zeros(self.total // 256, torch.uint8) for _ in range(2))
+        self.copy, self.copies, self._copy_type = None, None, F32
+        if copy_dtype is not None:
+            self.copy, self._copy_type = zeros(self.total, copy_dtype), _type(copy_dtype)
+            self.copies = [self.copy[a:a + p.numel()].view(p.shape)
+                           for a, p in zip(self.first, self.params)]
+            for c, p in zip(self.copies, self.params):
+                c.copy_(p)
+
+    def step(self, grads, lr=None):
+        """One step for the gradients (in the order of the parameters); ``lr``
+        replaces the rate for this step."""
+        if len(grads) != len(self.params):
+            raise CgtpError(f"{len(grads)} gradients for {len(self.params)} parameters")
+        gtype = grads[0].dtype
+        table = (_AdamwTensor * len(grads))()
+        for t, p, g in zip(table, self.params, grads):
+            if g.dtype != gtype or g.shape != p.shape or not g.is_cuda or not g.is_contiguous():
+                raise CgtpError(f"a gradient is {g.dtype} {tuple(g.shape)} on {g.device}"
+                                f"{'' if g.is_contiguous() else ', not contiguous'}; expected "
+                                f"contiguous {gtype} {tuple(p.shape)}")
+            t.param, t.grad, t.numel = p.data_ptr(), g.data_ptr(), p.numel()
+        args = _AdamwArgs(self.lr if lr is None else float(lr), *self.betas, self.eps,
+                          self.weight_decay, self.step_count + 1, self.seed)
+        _check(lib().cgtp_adamw_step(_type(self.dtype), _type(gtype), self.state_bits, len(grads),
+                                     table, _ptr(self.m), _ptr(self.v), _ptr(self.m_exp),
+                                     _ptr(self.v_exp), _ptr(self.copy), self._copy_type,
+                                     ctypes.byref(args), _stream()))
+        self.step_count += 1
+
+    def state_values(self, dtype=torch.bfloat16):
+        """(m, v), flat, as the values that 8-bit states stand for: exact in
+        bfloat16 and in fp32."""
+        if self.state_bits != 8:
+            raise CgtpError("state_values() is for 8-bit states")
+        m, v = (torch.empty(self.total, dtype=dtype, device=self.device) for _ in range(2))
+        _check(lib().cgtp_adamw_values(self.total, _ptr(self.m), _ptr(self.m_exp), _ptr(self.v),
+                                       _ptr(self.v_exp), _type(dtype), _ptr(m), _ptr(v),
+                                       _stream()))
+        return m, v

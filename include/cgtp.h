@@ -70,7 +70,10 @@ typedef enum {
     CGTP_E_DEVICE = 9       /* a kernel reported an error flag */
 } cgtp_status;
 
-typedef enum { CGTP_F32 = 0, CGTP_F64 = 1 } cgtp_dtype;
+/* CGTP_BF16 and CGTP_F16 are storage types of the training operators (the
+ * embedding, the norm and AdamW); the other entry points take CGTP_F32 and
+ * CGTP_F64 and refuse them (CGTP_E_ARG). */
+typedef enum { CGTP_F32 = 0, CGTP_F64 = 1, CGTP_BF16 = 2, CGTP_F16 = 3 } cgtp_dtype;
 typedef enum { CGTP_W_PER_EDGE = 0, CGTP_W_SHARED = 1 } cgtp_wmode;
 
 /* One tensor-product path: irrep indices into in1, in2, out; mode "uvu". */
@@ -538,6 +541,145 @@ cgtp_status cgtp_radial_path(cgtp_dtype dtype, int n_basis, int hidden, int64_t 
  * 1 when a bounded wait of the tensor-core kernel timed out (its output is then
  * incomplete). */
 cgtp_status cgtp_radial_device_status(int* code);
+
+/* ------------------------------------------------------ embedding ------ */
+/* First node features from a table of rows, one per chemical element (or any
+ * other index): out[n] = scale * table[index[n]] for n < N, rows of D elements.
+ * table [V, D] contiguous; out rows out_stride elements apart (>= D: out may be
+ * the scalar block of wider feature rows; the rest of a row is not touched).
+ * dtype: CGTP_F32, _F64, _BF16 or _F16 for table and out; products in fp32
+ * (fp64), rounded once.  index_bits: 32 or 64 (signed integers).  A negative
+ * index marks padding: its row is zero.  An index of V or more also gives a
+ * zero row, reads nothing, and sets the flag that cgtp_embed_device_status
+ * returns.  0 <= N, V < 2^31, D >= 1. */
+cgtp_status cgtp_embed_forward(cgtp_dtype dtype, int index_bits, int64_t N, int64_t V, int64_t D,
+                               const void* index, const void* table, double scale, void* out,
+                               int64_t out_stride, cgtp_stream stream);
+/* Its gradient: grad_table[v] = scale * sum over n with index[n] = v of
+ * grad_out[n]; every row of grad_table [V, D] is written (zero where no index
+ * points).  The indices are sorted on the device and each row's sum is taken in
+ * the order of n within fixed groups: the same inputs give the same bits.  Sums
+ * in fp32 (fp64), rounded once.  Padding and out-of-range indices as above.
+ * grad_out rows grad_stride >= 0 elements apart (0: one row for all).  workspace: device, caller-owned,
+ * 256-byte aligned, at least cgtp_embed_backward_workspace() bytes, contents
+ * need not be set. */
+cgtp_status cgtp_embed_backward(cgtp_dtype dtype, int index_bits, int64_t N, int64_t V, int64_t D,
+                                const void* index, const void* grad_out, int64_t grad_stride,
+                                double scale, void* grad_table, void* workspace,
+                                size_t workspace_bytes, cgtp_stream stream);
+cgtp_status cgtp_embed_backward_workspace(cgtp_dtype dtype, int64_t N, int64_t V, int64_t D,
+                                          size_t* bytes);
+/* *code = 1 if an index of V or more was met since the last query, then
+ * cleared.  Synchronous. */
+cgtp_status cgtp_embed_device_status(int* code);
+
+/* --------------------------------------- norms and gated residuals ------ */
+/* Equivariant RMS norm of feature rows and the residual update around an
+ * interaction block.  For each row and irrep (mul channels u, components m,
+ * D = (2l+1) mul elements):
+ *   norm(b)[m,u] = b[m,u] weight[u] / sqrt(sum b^2 / D + eps)
+ *   h = x + scale[u] sigmoid(gate[u]) norm(b)      (cgtp_residual_forward)
+ *   y = norm(h) with next_weight                   (the next block's input)
+ * weight, scale and next_weight hold one value per irrep and channel
+ * [channels], gate one per row, irrep and channel [n, channels]; a factor never
+ * depends on m, so the operations commute with rotations.  An irreps string of
+ * one "Dx0e" is the plain RMS norm of rows of D.
+ * Rows are stored as dtype (CGTP_F32, _F64, _BF16, _F16) and computed on in
+ * fp32 (fp64), rounded once; weight, scale, next_weight and their gradients are
+ * fp32 (fp64 for CGTP_F64).  y takes h as it is stored.  Values above 1e18 in
+ * magnitude overflow the sum of squares in fp32.  At most 32 irreps, l <= 6;
+ * eps > 0.  A cgtp_rows names rows `stride` elements apart (any stride where
+ * outputs do not overlap; data NULL: absent).  Rows, weights and multiplicities
+ * that allow 16-byte accesses (8-byte ones for 16-bit types) take the faster
+ * kernels.  Host only to create; the handle is immutable and may be shared
+ * between threads. */
+typedef struct {
+    void* data; /* inputs are only read */
+    int64_t stride;
+} cgtp_rows;
+typedef struct cgtp_norm_s* cgtp_norm;
+cgtp_status cgtp_norm_create(cgtp_norm* out, const char* irreps, double eps, cgtp_dtype dtype);
+cgtp_status cgtp_norm_destroy(cgtp_norm norm);
+/* Row width; values per row of weights and gates. */
+cgtp_status cgtp_norm_info(cgtp_norm norm, int64_t* dim, int64_t* channels);
+/* y = norm(x) (weight NULL: ones).  y may be x. */
+cgtp_status cgtp_norm_forward(cgtp_norm norm, int64_t n, cgtp_rows x, const void* weight,
+                              cgtp_rows y, cgtp_stream stream);
+/* h and y as above.  x, gate, scale, weight, next_weight may be NULL (no
+ * addend, 1, 1, 1, 1); y NULL: not computed.  h may be x or b; y may not be h. */
+cgtp_status cgtp_residual_forward(cgtp_norm norm, int64_t n, cgtp_rows x, cgtp_rows b,
+                                  const void* weight, cgtp_rows gate, const void* scale,
+                                  const void* next_weight, cgtp_rows h, cgtp_rows y,
+                                  cgtp_stream stream);
+/* Bytes of device scratch for the weight gradients below (one partial row of
+ * channel sums per CTA, added in fixed order: deterministic). */
+cgtp_status cgtp_norm_workspace(cgtp_norm norm, size_t* bytes);
+/* Gradient of cgtp_norm_forward: grad_x, grad_weight (either NULL: not
+ * computed).  workspace (256-byte aligned, cgtp_norm_workspace() bytes, need not
+ * be set) is required with grad_weight. */
+cgtp_status cgtp_norm_backward(cgtp_norm norm, int64_t n, cgtp_rows x, const void* weight,
+                               cgtp_rows grad_y, cgtp_rows grad_x, void* grad_weight,
+                               void* workspace, size_t workspace_bytes, cgtp_stream stream);
+/* Gradient of cgtp_residual_forward for the cotangents grad_h and grad_y (one of
+ * them may be NULL: zero); h as the forward pass stored it (NULL if grad_y is).
+ * grad_x is the whole gradient of h, which is x's.  Every output may be NULL;
+ * outputs may not be inputs.  workspace as above, required with grad_weight,
+ * grad_scale or grad_next_weight. */
+cgtp_status cgtp_residual_backward(cgtp_norm norm, int64_t n, cgtp_rows b, cgtp_rows h,
+                                   const void* weight, cgtp_rows gate, const void* scale,
+                                   const void* next_weight, cgtp_rows grad_h, cgtp_rows grad_y,
+                                   cgtp_rows grad_x, cgtp_rows grad_b, cgtp_rows grad_gate,
+                                   void* grad_weight, void* grad_scale, void* grad_next_weight,
+                                   void* workspace, size_t workspace_bytes, cgtp_stream stream);
+
+/* ---------------------------------------------------------- AdamW ------ */
+/* One optimiser step over all parameters of a network (decoupled weight decay):
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps)
+ * The moments of all tensors lie in flat arrays, tensor i's at first[i]
+ * (cgtp_adamw_layout; every tensor starts on a block of CGTP_ADAMW_BLOCK
+ * elements and the last block is filled up with zeros). */
+#define CGTP_ADAMW_BLOCK 256
+typedef struct {
+    void* param; /* updated in place */
+    const void* grad;
+    int64_t numel;
+} cgtp_adamw_tensor;
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;  /* 1 at the first step */
+    uint64_t seed; /* of the stochastic rounding of 8-bit states */
+} cgtp_adamw_args;
+/* first [n] (may be NULL) and the total length of a flat array, in elements. */
+cgtp_status cgtp_adamw_layout(int n, const int64_t* numel, int64_t* first, int64_t* total);
+/* Types: param CGTP_F32 with a gradient of CGTP_F32, _BF16 or _F16; CGTP_F64,
+ * CGTP_BF16 or CGTP_F16 with their own.  Arithmetic in fp32 (fp64).
+ * state_bits 32: m and v [total] in fp32 (fp64 for CGTP_F64), m_exp and v_exp
+ * unused.  state_bits 8 (not CGTP_F64: CGTP_E_UNSUPPORTED): one byte per element
+ * and one exponent byte per block in m_exp and v_exp [total / 256].  m: sign
+ * (bit 7), exponent field e (4 bits), fraction f (3 bits), standing for
+ * (e ? (8 + f) 2^(e-1) : f) 2^(x - 128 - 18); v: e of 5 bits, no sign,
+ * 2^(x - 128 - 34); x the exponent byte, 255 for a block in which an infinity
+ * or a NaN was met (all of it reads as NaN).  Values are rounded to a neighbour
+ * with probability by distance, from a hash of (seed, step, i, element); a
+ * positive v never becomes zero.  Zero-filled states are fresh ones in either
+ * form.
+ * copy (may be NULL): [total] in copy_dtype (CGTP_BF16 or CGTP_F16), the
+ * parameters rounded to nearest in the flat layout, as plans with 16-bit
+ * weights read them; not for CGTP_F64.  Tensors may have any element-aligned
+ * address; flat arrays are 256-byte aligned.  eps > 0, 0 <= beta < 1, step >= 1.
+ * One launch per 64 tensors.  The scalars are passed by value: a captured graph
+ * repeats the step number it was captured with. */
+cgtp_status cgtp_adamw_step(cgtp_dtype param_dtype, cgtp_dtype grad_dtype, int state_bits, int n,
+                            const cgtp_adamw_tensor* tensors, void* m, void* v, uint8_t* m_exp,
+                            uint8_t* v_exp, void* copy, cgtp_dtype copy_dtype,
+                            const cgtp_adamw_args* args, cgtp_stream stream);
+/* The values that 8-bit states stand for, exactly, as CGTP_F32 or CGTP_BF16
+ * arrays [total] (256-byte aligned). */
+cgtp_status cgtp_adamw_values(int64_t total, const void* m, const uint8_t* m_exp, const void* v,
+                              const uint8_t* v_exp, cgtp_dtype out_dtype, void* m_out, void* v_out,
+                              cgtp_stream stream);
 
 /* ------------------------------------------------------------ misc ------ */
 const char* cgtp_status_str(cgtp_status s);
