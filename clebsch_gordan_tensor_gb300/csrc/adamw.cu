@@ -146,15 +146,14 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
         const int64_t at = (int64_t)b * kBlock;
         const bool whole = left >= kBlock && (uintptr_t)p % (sizeof(P) * V) == 0 &&
                            (uintptr_t)g % (sizeof(G) * V) == 0;
-        Pack<P, V> pp[NV];
-        C gg[NV][V], m[NV][V], v[NV][V];
+        C pn[NV][V], gg[NV][V], m[NV][V], v[NV][V];
         if (whole) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                pp[j] = load_pack<P, V>(p + (j * 32 + lane) * V);
+                const Pack<P, V> pp = load_pack<P, V>(p + (j * 32 + lane) * V);
                 const Pack<G, V> gp = load_pack<G, V>(g + (j * 32 + lane) * V);
 #pragma unroll
-                for (int i = 0; i < V; ++i) gg[j][i] = (C)widen(gp.v[i]);
+                for (int i = 0; i < V; ++i) pn[j][i] = pp.get(i), gg[j][i] = (C)gp.get(i);
             }
         } else {
 #pragma unroll
@@ -162,7 +161,7 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const int k = (j * 32 + lane) * V + i;
-                    pp[j].v[i] = k < left ? p[k] : narrow<P>((C)0);
+                    pn[j][i] = k < left ? (C)widen(p[k]) : (C)0;
                     gg[j][i] = k < left ? (C)widen(g[k]) : (C)0;
                 }
         }
@@ -185,7 +184,7 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
                 const int64_t k = at + (j * 32 + lane) * V;
                 const Pack<C, V> mp = load_pack<C, V>((C*)m_ + k), vp = load_pack<C, V>((C*)v_ + k);
 #pragma unroll
-                for (int i = 0; i < V; ++i) m[j][i] = mp.v[i], v[j][i] = vp.v[i];
+                for (int i = 0; i < V; ++i) m[j][i] = mp.get(i), v[j][i] = vp.get(i);
             }
         }
         uint32_t mtop = 0, vtop = 0;
@@ -195,8 +194,7 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
             for (int i = 0; i < V; ++i) {
                 m[j][i] = ema(m[j][i], a.b1, gg[j][i], a.c1);
                 v[j][i] = ema(v[j][i], a.b2, square(gg[j][i]), a.c2);
-                const C pn = stepped((C)widen(pp[j].v[i]), m[j][i], v[j][i], a);
-                pp[j].v[i] = narrow<P>(pn);
+                pn[j][i] = stepped(pn[j][i], m[j][i], v[j][i], a);
                 if constexpr (EIGHT) {
                     mtop = max(mtop, __float_as_uint(m[j][i]) & 0x7FFFFFFFu);
                     vtop = max(vtop, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
@@ -205,27 +203,38 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
         }
         if (whole) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) store_pack(p + (j * 32 + lane) * V, pp[j]);
+            for (int j = 0; j < NV; ++j) {
+                Pack<P, V> pp;
+                pp.set(pn[j]);
+                store_pack(p + (j * 32 + lane) * V, pp);
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const int k = (j * 32 + lane) * V + i;
-                    if (k < left) p[k] = pp[j].v[i];
+                    if (k < left) p[k] = narrow<P>(pn[j][i]);
                 }
         }
-        if (copy_kind != 0) {
+        if constexpr (sizeof(C) == 4) {
+            if (copy_kind != 0) {  // of the parameter as it is stored
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                Pack<uint16_t, V> c;
+                for (int j = 0; j < NV; ++j) {
+                    float x[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float x = (float)widen(pp[j].v[i]);
-                    c.v[i] = copy_kind == 1 ? __bfloat16_as_ushort(__float2bfloat16_rn(x))
-                                            : __half_as_ushort(__float2half_rn(x));
+                    for (int i = 0; i < V; ++i) x[i] = widen(narrow<P>(pn[j][i]));
+                    const int64_t k = at + (j * 32 + lane) * V;
+                    Pack<__nv_bfloat16, V> b;
+                    Pack<__half, V> h;
+                    if (copy_kind == 1) {
+                        b.set(x);
+                        store_pack((__nv_bfloat16*)copy + k, b);
+                    } else {
+                        h.set(x);
+                        store_pack((__half*)copy + k, h);
+                    }
                 }
-                store_pack(copy + at + (j * 32 + lane) * V, c);
             }
         }
         if constexpr (EIGHT) {
@@ -258,8 +267,8 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
             for (int j = 0; j < NV; ++j) {
                 const int64_t k = at + (j * 32 + lane) * V;
                 Pack<C, V> mp, vp;
-#pragma unroll
-                for (int i = 0; i < V; ++i) mp.v[i] = m[j][i], vp.v[i] = v[j][i];
+                mp.set(m[j]);
+                vp.set(v[j]);
                 store_pack((C*)m_ + k, mp);
                 store_pack((C*)v_ + k, vp);
             }
@@ -278,14 +287,17 @@ adamw_values_kernel(int64_t quads, const uint32_t* __restrict__ mc,
          q += (int64_t)gridDim.x * 256) {
         const float ms = block_scale(me[q / (kBlock / 4)]), vs = block_scale(ve[q / (kBlock / 4)]);
         const uint32_t a = mc[q], b = vc[q];
-        Pack<O, 4> x, y;
+        float xm[4], xv[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            x.v[i] = narrow<O>(decode_m(a >> 8 * i & 0xFFu, ms));
-            y.v[i] = narrow<O>(decode_v(b >> 8 * i & 0xFFu, vs));
+            xm[i] = decode_m(a >> 8 * i & 0xFFu, ms);
+            xv[i] = decode_v(b >> 8 * i & 0xFFu, vs);
         }
-        store_pack(m + 4 * q, x);
-        store_pack(v + 4 * q, y);
+        Pack<O, 4> pm, pv;
+        pm.set(xm);
+        pv.set(xv);
+        store_pack(m + 4 * q, pm);
+        store_pack(v + 4 * q, pv);
     }
 }
 

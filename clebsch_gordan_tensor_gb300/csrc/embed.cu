@@ -38,15 +38,17 @@ embed_forward_kernel(int64_t n, int64_t v, int64_t d, int T, int64_t tiles,
         if (col >= d) continue;
         const int64_t i = index[row];
         Pack<S, V> p;
+        typename Compute<S>::type x[V];
         if (i >= 0 && i < v) {
             p = load_pack<S, V>(table + i * d + col);
 #pragma unroll
-            for (int k = 0; k < V; ++k) p.v[k] = narrow<S>(widen(p.v[k]) * scale);
+            for (int k = 0; k < V; ++k) x[k] = p.get(k) * scale;
         } else {
             if (i >= v && t == 0) cgtp_embed_error = 1;
 #pragma unroll
-            for (int k = 0; k < V; ++k) p.v[k] = narrow<S>((typename Compute<S>::type)0);
+            for (int k = 0; k < V; ++k) x[k] = 0;
         }
+        p.set(x);
         store_pack(out + row * stride + col, p);
     }
 }
@@ -197,7 +199,8 @@ embed_sum_kernel(uint32_t n, uint32_t v, int64_t d, int T, uint32_t tiles, uint3
         } else {
             Pack<S, V> o;
 #pragma unroll
-            for (int k = 0; k < V; ++k) o.v[k] = narrow<S>(acc[k] * scale);
+            for (int k = 0; k < V; ++k) acc[k] *= scale;
+            o.set(acc);
             store_pack(table + (int64_t)cur * d + col, o);
         }
     };
@@ -222,7 +225,7 @@ embed_sum_kernel(uint32_t n, uint32_t v, int64_t d, int T, uint32_t tiles, uint3
                 for (int k = 0; k < V; ++k) acc[k] = 0;
             }
 #pragma unroll
-            for (int k = 0; k < V; ++k) acc[k] += widen(row[u].v[k]);
+            for (int k = 0; k < V; ++k) acc[k] += row[u].get(k);
         }
     }
     finish(last < n && keys[last] == cur);
@@ -258,7 +261,8 @@ embed_join_kernel(uint32_t n, uint32_t v, int64_t d, int T, uint32_t tiles, uint
     }
     Pack<S, V> o;
 #pragma unroll
-    for (int k = 0; k < V; ++k) o.v[k] = narrow<S>(acc[k] * scale);
+    for (int k = 0; k < V; ++k) acc[k] *= scale;
+    o.set(acc);
     store_pack(table + (int64_t)cur * d + col, o);
 }
 

@@ -141,12 +141,14 @@ struct NormTable {
     int n = 0, ctas = 0;
 };
 struct NormForward {
+    static constexpr int kThreads = 256, kInputs = 3;  // of a CTA; tensors read
     int64_t n;
     double eps;
     cgtp_rows b, x, gate, h, y;
     const void *weight, *scale, *next_weight;
 };
 struct NormBackward {
+    static constexpr int kThreads = 128, kInputs = 5;
     int64_t n;
     double eps;
     cgtp_rows b, h, gate, grad_h, grad_y, grad_x, grad_b, grad_gate;
@@ -155,12 +157,12 @@ struct NormBackward {
     void* partial;  // NULL: no weight gradients
     int channels;
 };
-// vectors: every row, weight and multiplicity allows 16-byte accesses (8-byte
-// ones for 16-bit storage).
+// vector: the channels (1, 2, 4 or 8, 16 bytes at most) by which every row and
+// multiplicity can be read at once.
 #define CGTP_NORM_DECL(t)                                                                  \
-    cudaError_t launch_norm_forward_##t(const NormTable&, const NormForward&, bool vectors, \
+    cudaError_t launch_norm_forward_##t(const NormTable&, const NormForward&, int vector,  \
                                         cudaStream_t);                                      \
-    cudaError_t launch_norm_backward_##t(const NormTable&, const NormBackward&, bool vectors, \
+    cudaError_t launch_norm_backward_##t(const NormTable&, const NormBackward&, int vector, \
                                          cudaStream_t);
 CGTP_NORM_DECL(f32)
 CGTP_NORM_DECL(f64)

@@ -3,13 +3,13 @@
 
 namespace cgtp {
 
-cudaError_t launch_norm_forward_f16(const NormTable& tab, const NormForward& a, bool vectors,
-                                   cudaStream_t s) {
-    return forward<__half>(tab, a, vectors, s);
-}
-cudaError_t launch_norm_backward_f16(const NormTable& tab, const NormBackward& a, bool vectors,
+cudaError_t launch_norm_forward_f16(const NormTable& tab, const NormForward& a, int vector,
                                     cudaStream_t s) {
-    return backward<__half>(tab, a, vectors, s);
+    return launch_norm<__half>(tab, a, vector, s);
+}
+cudaError_t launch_norm_backward_f16(const NormTable& tab, const NormBackward& a, int vector,
+                                     cudaStream_t s) {
+    return launch_norm<__half>(tab, a, vector, s);
 }
 
 }  // namespace cgtp

@@ -22,7 +22,8 @@
 // two reductions, so every tensor is read once and written once.  A CTA stays
 // with one irrep: its threads keep their channels' weights in registers, and in
 // the gradient their channels' sums, which leave as one partial row per CTA.
-// Both directions are bound by HBM.
+// gweight and gscale share one sum, A[c] = sum over rows of sigmoid(z) P: they
+// are scale A and weight A.  Both directions are bound by HBM.
 #pragma once
 
 #include <algorithm>
@@ -34,11 +35,25 @@ namespace cgtp {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kMaxWarps = 16;
+
+// Channels of one access for degree l.  Above l = 1 a thread holds 2l+1 >= 5
+// vectors of every tensor; with eight 16-bit channels each they would not stay
+// in registers.
+template <int V, int L>
+constexpr int kWidth = V == 8 && L > 1 ? 4 : V;
 
 __device__ __forceinline__ float rsqrt_of(float x) { return rsqrtf(x); }
 __device__ __forceinline__ double rsqrt_of(double x) { return 1.0 / sqrt(x); }
-__device__ __forceinline__ float sigmoid_of(float z) { return 1.f / (1.f + expf(-z)); }
+// The special-function unit's 2^x and 1/x: together below 1e-6 of the result for
+// |z| <= 10, where a gate still moves.  Flushing subnormals only touches
+// sigmoids below 1e-38, and sigmoid(inf) is 1, which absent gates stand for.
+__device__ __forceinline__ float sigmoid_of(float z) {
+    float e, q;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.f + e));
+    return q;
+}
 __device__ __forceinline__ double sigmoid_of(double z) { return 1.0 / (1.0 + exp(-z)); }
 
 // Sums of R <= 3 values over the T threads of a group, the same on all of them
@@ -47,7 +62,7 @@ __device__ __forceinline__ double sigmoid_of(double z) { return 1.0 / (1.0 + exp
 // the call in between, which every thread reaches after its reads.
 template <typename C>
 struct GroupSum {
-    C (*buf)[kThreads / 32];  // [2][3][warps]
+    C (*buf)[kMaxWarps];  // [2][3][warps]
     int T, flip = 0;
     template <int R>
     __device__ void operator()(C (&v)[R]) {
@@ -57,18 +72,20 @@ struct GroupSum {
             for (int r = 0; r < R; ++r) v[r] += __shfl_xor_sync(0xFFFFFFFFu, v[r], o);
         if (T <= 32) return;
         const int warp = threadIdx.x >> 5, nw = T >> 5, first = warp / nw * nw;
-        C (*const side)[kThreads / 32] = buf + flip * 3;
+        C (*const side)[kMaxWarps] = buf + flip * 3;
         flip ^= 1;
         if ((threadIdx.x & 31) == 0)
 #pragma unroll
             for (int r = 0; r < R; ++r) side[r][warp] = v[r];
         __syncthreads();
+        // nw, a power of two, partial sums, over the lanes again: a loop over
+        // them took a third of a wide row's time
+        const int at = first + (threadIdx.x & (nw - 1));
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            C s = 0;
-            for (int w = 0; w < nw; ++w) s += side[r][first + w];
-            v[r] = s;
-        }
+        for (int r = 0; r < R; ++r) v[r] = side[r][at];
+        for (int o = nw >> 1; o > 0; o >>= 1)
+#pragma unroll
+            for (int r = 0; r < R; ++r) v[r] += __shfl_xor_sync(0xFFFFFFFFu, v[r], o);
     }
 };
 
@@ -78,14 +95,55 @@ __device__ __forceinline__ void load_param(C (&out)[V], const C* p, int at, C mi
     for (int i = 0; i < V; ++i) out[i] = p ? p[at + i] : missing;
 }
 
+// Rows of one tensor at an irrep; NULL where the tensor is absent.
+template <typename S>
+__device__ __forceinline__ S* row_of(const cgtp_rows& q, int64_t row, int at) {
+    return q.data ? (S*)q.data + row * q.stride + at : nullptr;
+}
+
 // ------------------------------------------------------------- forward --
 
 template <typename S, int V, int L, int K>
+struct ForwardRegs {
+    Pack<S, V> b[K][2 * L + 1], x[K][2 * L + 1], z[K];
+    // What absent tensors and threads without a row stand for, so that the
+    // arithmetic has no branches.
+    __device__ __forceinline__ ForwardRegs() {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            z[k].fill(INFINITY);
+#pragma unroll
+            for (int m = 0; m < 2 * L + 1; ++m) b[k][m].fill(0), x[k][m].fill(0);
+        }
+    }
+};
+
+template <typename S, int V, int L, int K>
+__device__ __forceinline__ void load_forward(ForwardRegs<S, V, L, K>& q, const NormIrrep& ir,
+                                             const NormForward& a, int64_t row, int t) {
+    if (row >= a.n) return;
+    const S* b = row_of<const S>(a.b, row, ir.off);
+    const S* x = row_of<const S>(a.x, row, ir.off);
+    const S* z = row_of<const S>(a.gate, row, ir.ch);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (t + k * ir.T < ir.mul / V) {
+            const int u = (t + k * ir.T) * V;
+#pragma unroll
+            for (int m = 0; m < 2 * L + 1; ++m) {
+                q.b[k][m] = load_pack<S, V>(b + m * ir.mul + u);
+                if (x) q.x[k][m] = load_pack<S, V>(x + m * ir.mul + u);
+            }
+            if (z) q.z[k] = load_pack<S, V>(z + u);
+        }
+}
+
+template <typename S, int V, int L, int K>
 __device__ __forceinline__ void forward_body(const NormIrrep& ir, int cta, const NormForward& a,
-                                             typename Compute<S>::type (*sums)[kThreads / 32]) {
+                                             typename Compute<S>::type (*sums)[kMaxWarps]) {
     using C = typename Compute<S>::type;
     constexpr int M = 2 * L + 1;
-    const int T = ir.T, t = threadIdx.x % T, G = kThreads / T;
+    const int T = ir.T, t = threadIdx.x % T, G = blockDim.x / T;
     const int U = ir.mul / V;
     const C inv_d = (C)1 / (C)(M * ir.mul), eps = (C)a.eps;
     const C *w = (const C*)a.weight, *sc = (const C*)a.scale, *w2 = (const C*)a.next_weight;
@@ -99,78 +157,65 @@ __device__ __forceinline__ void forward_body(const NormIrrep& ir, int cta, const
         for (int i = 0; i < V; ++i) coef[k][i] *= sc ? sc[c + i] : (C)1;
     }
     GroupSum<C> sum{sums, T};
-    for (int64_t base = (int64_t)cta * G; base < a.n; base += (int64_t)ir.ctas * G) {
-        const int64_t row = base + threadIdx.x / T;
+    const int64_t step = (int64_t)ir.ctas * G;
+    int64_t row = (int64_t)cta * G + threadIdx.x / T;
+    // scalar rows are short: the next one is on its way during the sums
+    constexpr bool kAhead = L == 0 && K * V <= 8;
+    ForwardRegs<S, V, L, K> q, ahead;
+    load_forward(q, ir, a, row, t);
+    for (int64_t base = (int64_t)cta * G; base < a.n; base += step, row += step) {
+        if constexpr (kAhead) load_forward(ahead, ir, a, row + step, t);
         const bool in = row < a.n;
-        const S* b = (const S*)a.b.data + row * a.b.stride + ir.off;
-        const S* x = a.x.data ? (const S*)a.x.data + row * a.x.stride + ir.off : nullptr;
-        const S* z = a.gate.data ? (const S*)a.gate.data + row * a.gate.stride + ir.ch : nullptr;
-        Pack<S, V> bp[K][M], xp[K][M], zp[K];
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const bool on = in && t + k * T < U;
-            const int u = (t + k * T) * V;
-#pragma unroll
-            for (int m = 0; m < M; ++m) {
-                if (on) {
-                    bp[k][m] = load_pack<S, V>(b + m * ir.mul + u);
-                    if (x) xp[k][m] = load_pack<S, V>(x + m * ir.mul + u);
-                }
-            }
-            if (on && z) zp[k] = load_pack<S, V>(z + u);
-        }
         C s[1] = {0};
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (in && t + k * T < U)
 #pragma unroll
-                for (int m = 0; m < M; ++m)
+            for (int m = 0; m < M; ++m)
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const C v = widen(bp[k][m].v[i]);
-                        s[0] += v * v;
-                    }
+                for (int i = 0; i < V; ++i) s[0] += q.b[k][m].get(i) * q.b[k][m].get(i);
         sum(s);
         const C r = rsqrt_of(s[0] * inv_d + eps);
         s[0] = 0;
-        S* h = (S*)a.h.data + row * a.h.stride + ir.off;
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (in && t + k * T < U) {
                 C f[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    f[i] = r * coef[k][i];
-                    if (z) f[i] *= sigmoid_of(widen(zp[k].v[i]));
-                }
+                for (int i = 0; i < V; ++i) f[i] = r * coef[k][i] * sigmoid_of(q.z[k].get(i));
+                S* h = row_of<S>(a.h, row, ir.off);
 #pragma unroll
                 for (int m = 0; m < M; ++m) {
+                    C v[V];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        C v = f[i] * widen(bp[k][m].v[i]);
-                        if (x) v += widen(xp[k][m].v[i]);
-                        bp[k][m].v[i] = narrow<S>(v);
-                        v = widen(bp[k][m].v[i]);
-                        s[0] += v * v;
-                    }
-                    store_pack(h + m * ir.mul + (t + k * T) * V, bp[k][m]);
+                    for (int i = 0; i < V; ++i)
+                        v[i] = f[i] * q.b[k][m].get(i) + q.x[k][m].get(i);
+                    q.b[k][m].set(v);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) s[0] += q.b[k][m].get(i) * q.b[k][m].get(i);
+                    store_pack(h + m * ir.mul + (t + k * T) * V, q.b[k][m]);
                 }
             }
         if (a.y.data) {
             sum(s);
             const C r2 = rsqrt_of(s[0] * inv_d + eps);
-            S* y = (S*)a.y.data + row * a.y.stride + ir.off;
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (in && t + k * T < U)
+                if (in && t + k * T < U) {
+                    S* y = row_of<S>(a.y, row, ir.off);
 #pragma unroll
                     for (int m = 0; m < M; ++m) {
+                        C v[V];
 #pragma unroll
-                        for (int i = 0; i < V; ++i)
-                            bp[k][m].v[i] = narrow<S>(widen(bp[k][m].v[i]) * r2 * next[k][i]);
-                        store_pack(y + m * ir.mul + (t + k * T) * V, bp[k][m]);
+                        for (int i = 0; i < V; ++i) v[i] = q.b[k][m].get(i) * (r2 * next[k][i]);
+                        q.b[k][m].set(v);
+                        store_pack(y + m * ir.mul + (t + k * T) * V, q.b[k][m]);
                     }
+                }
         }
+        if constexpr (kAhead)
+            q = ahead;
+        else
+            load_forward(q, ir, a, row + step, t);
     }
 }
 
@@ -179,27 +224,28 @@ __device__ __forceinline__ void forward_body(const NormIrrep& ir, int cta, const
 // second read comes from L2.
 template <typename S, int V>
 __device__ void forward_wide(const NormIrrep& ir, int cta, const NormForward& a,
-                             typename Compute<S>::type (*sums)[kThreads / 32]) {
+                             typename Compute<S>::type (*sums)[kMaxWarps]) {
     using C = typename Compute<S>::type;
     const int M = 2 * ir.l + 1, U = ir.mul / V;
     const C inv_d = (C)1 / ((C)M * (C)ir.mul), eps = (C)a.eps;
     const C *w = (const C*)a.weight, *sc = (const C*)a.scale, *w2 = (const C*)a.next_weight;
-    GroupSum<C> sum{sums, kThreads};
+    const int B = blockDim.x;
+    GroupSum<C> sum{sums, B};
     for (int64_t row = cta; row < a.n; row += ir.ctas) {
         const S* b = (const S*)a.b.data + row * a.b.stride + ir.off;
         const S* x = a.x.data ? (const S*)a.x.data + row * a.x.stride + ir.off : nullptr;
         const S* z = a.gate.data ? (const S*)a.gate.data + row * a.gate.stride + ir.ch : nullptr;
         S* h = (S*)a.h.data + row * a.h.stride + ir.off;
         C s[1] = {0};
-        for (int64_t e = threadIdx.x; e < (int64_t)M * U; e += kThreads) {
+        for (int64_t e = threadIdx.x; e < (int64_t)M * U; e += B) {
             const Pack<S, V> p = load_pack<S, V>(b + e * V);
 #pragma unroll
-            for (int i = 0; i < V; ++i) s[0] += widen(p.v[i]) * widen(p.v[i]);
+            for (int i = 0; i < V; ++i) s[0] += p.get(i) * p.get(i);
         }
         sum(s);
         const C r = rsqrt_of(s[0] * inv_d + eps);
         s[0] = 0;
-        for (int u = threadIdx.x; u < U; u += kThreads) {
+        for (int u = threadIdx.x; u < U; u += B) {
             const int c = ir.ch + u * V;
             C f[V];
             load_param(f, w, c, (C)1);
@@ -212,13 +258,15 @@ __device__ void forward_wide(const NormIrrep& ir, int cta, const NormForward& a,
                 const int64_t at = (int64_t)m * ir.mul + (int64_t)u * V;
                 Pack<S, V> p = load_pack<S, V>(b + at), q;
                 if (x) q = load_pack<S, V>(x + at);
+                C v[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    C v = f[i] * widen(p.v[i]);
-                    if (x) v += widen(q.v[i]);
-                    p.v[i] = narrow<S>(v);
-                    s[0] += widen(p.v[i]) * widen(p.v[i]);
+                    v[i] = f[i] * p.get(i);
+                    if (x) v[i] += q.get(i);
                 }
+                p.set(v);
+#pragma unroll
+                for (int i = 0; i < V; ++i) s[0] += p.get(i) * p.get(i);
                 store_pack(h + at, p);
             }
         }
@@ -226,14 +274,16 @@ __device__ void forward_wide(const NormIrrep& ir, int cta, const NormForward& a,
             sum(s);
             const C r2 = rsqrt_of(s[0] * inv_d + eps);
             S* y = (S*)a.y.data + row * a.y.stride + ir.off;
-            for (int u = threadIdx.x; u < U; u += kThreads) {
+            for (int u = threadIdx.x; u < U; u += B) {
                 C f[V];
                 load_param(f, w2, ir.ch + u * V, (C)1);
                 for (int m = 0; m < M; ++m) {  // the thread's own stores to h
                     const int64_t at = (int64_t)m * ir.mul + (int64_t)u * V;
                     Pack<S, V> p = load_pack<S, V>(h + at);
+                    C v[V];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) p.v[i] = narrow<S>(widen(p.v[i]) * r2 * f[i]);
+                    for (int i = 0; i < V; ++i) v[i] = p.get(i) * (r2 * f[i]);
+                    p.set(v);
                     store_pack(y + at, p);
                 }
             }
@@ -242,184 +292,212 @@ __device__ void forward_wide(const NormIrrep& ir, int cta, const NormForward& a,
 }
 
 // LC: the largest l a launch holds, in classes (0, 3 or 6), so that plain rows
-// do not carry the registers of 13 components.
-#define CGTP_NORM_BODIES(LC, CALL, WIDE)                          \
-    if (ir.K == 0) {                                              \
-        WIDE;                                                     \
-    } else if (ir.l == 0) {                                       \
-        if (ir.K == 1) { CALL(0, 1); }                            \
-        else if (ir.K == 2) { CALL(0, 2); }                       \
-        else if (ir.K == 4) { CALL(0, 4); }                       \
-        else { CALL(0, 8); }                                      \
-    }                                                             \
-    if constexpr (LC >= 3) {                                      \
-        if (ir.K != 0 && ir.l == 1) {                             \
-            if (ir.K == 1) { CALL(1, 1); } else { CALL(1, 2); }   \
-        }                                                         \
-        if (ir.K != 0 && ir.l == 2) { CALL(2, 1); }               \
-        if (ir.K != 0 && ir.l == 3) { CALL(3, 1); }               \
-    }                                                             \
-    if constexpr (LC >= 6) {                                      \
-        if (ir.K != 0 && ir.l == 4) { CALL(4, 1); }               \
-        if (ir.K != 0 && ir.l == 5) { CALL(5, 1); }               \
-        if (ir.K != 0 && ir.l == 6) { CALL(6, 1); }               \
+// do not carry the registers of 13 components; K: vectors of a thread, above 1
+// for plain rows only.
+#define CGTP_NORM_BODIES(LC, K, CALL, WIDE)     \
+    if (ir.K == 0) {                            \
+        WIDE;                                   \
+    } else if (ir.l == 0) {                     \
+        CALL(0, K);                             \
+    }                                           \
+    if constexpr (LC >= 3) {                    \
+        if (ir.K != 0) {                        \
+            if (ir.l == 1) CALL(1, 1);          \
+            if (ir.l == 2) CALL(2, 1);          \
+            if (ir.l == 3) CALL(3, 1);          \
+        }                                       \
+    }                                           \
+    if constexpr (LC >= 6) {                    \
+        if (ir.K != 0) {                        \
+            if (ir.l == 4) CALL(4, 1);          \
+            if (ir.l == 5) CALL(5, 1);          \
+            if (ir.l == 6) CALL(6, 1);          \
+        }                                       \
     }
 
-template <typename S, int V, int LC>
-__global__ void __launch_bounds__(kThreads)
+// Plain rows: 512 threads with 64 registers, two CTAs an SM (128 and one CTA
+// with more than one vector a thread).
+template <int LC, int K>
+constexpr int kForwardCtas = LC == 0 && K == 1 ? 2 : 1;
+
+template <typename S, int V, int LC, int K>
+__global__ void __launch_bounds__(LC == 0 ? 512 : 256, (kForwardCtas<LC, K>))
 norm_forward_kernel(const __grid_constant__ NormTable tab, const __grid_constant__ NormForward a) {
-    __shared__ typename Compute<S>::type sums[6][kThreads / 32];
+    __shared__ typename Compute<S>::type sums[6][kMaxWarps];
     int i = 0;
     while (i + 1 < tab.n && (int)blockIdx.x >= tab.ir[i + 1].cta0) ++i;
     const NormIrrep& ir = tab.ir[i];
     const int cta = blockIdx.x - ir.cta0;
-#define CALL(L, K) forward_body<S, V, L, K>(ir, cta, a, sums)
-    CGTP_NORM_BODIES(LC, CALL, (forward_wide<S, V>(ir, cta, a, sums)))
+#define CALL(L, K) forward_body<S, kWidth<V, L>, L, K>(ir, cta, a, sums)
+    CGTP_NORM_BODIES(LC, K, CALL, (forward_wide<S, V>(ir, cta, a, sums)))
 #undef CALL
 }
 
 // ------------------------------------------------------------ gradient --
 
-// The three channel sums of a CTA, [3][mul] at its place in the partial rows.
+// The two channel sums of a CTA (A and Q), [2][mul] at its place in the partial
+// rows.
 template <typename C>
 __device__ __forceinline__ C* partial_row(const NormIrrep& ir, int cta, const NormBackward& a) {
-    return (C*)a.partial + ir.part0 + (int64_t)cta * 3 * ir.mul;
+    return (C*)a.partial + ir.part0 + (int64_t)cta * 2 * ir.mul;
+}
+
+template <typename S, int V, int L, int K>
+struct BackwardRegs {
+    Pack<S, V> b[K][2 * L + 1], h[K][2 * L + 1], gh[K][2 * L + 1], gy[K][2 * L + 1], z[K];
+    __device__ __forceinline__ BackwardRegs() {  // see ForwardRegs
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            z[k].fill(INFINITY);
+#pragma unroll
+            for (int m = 0; m < 2 * L + 1; ++m)
+                b[k][m].fill(0), h[k][m].fill(0), gh[k][m].fill(0), gy[k][m].fill(0);
+        }
+    }
+};
+
+template <typename S, int V, int L, int K>
+__device__ __forceinline__ void load_backward(BackwardRegs<S, V, L, K>& q, const NormIrrep& ir,
+                                              const NormBackward& a, int64_t row, int t) {
+    if (row >= a.n) {  // adds nothing to the channel sums
+        q = BackwardRegs<S, V, L, K>();
+        return;
+    }
+    const S *b = row_of<const S>(a.b, row, ir.off), *h = row_of<const S>(a.h, row, ir.off);
+    const S *gh = row_of<const S>(a.grad_h, row, ir.off);
+    const S *gy = row_of<const S>(a.grad_y, row, ir.off);
+    const S* z = row_of<const S>(a.gate, row, ir.ch);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (t + k * ir.T < ir.mul / V) {
+            const int u = (t + k * ir.T) * V;
+#pragma unroll
+            for (int m = 0; m < 2 * L + 1; ++m) {
+                q.b[k][m] = load_pack<S, V>(b + m * ir.mul + u);
+                if (gh) q.gh[k][m] = load_pack<S, V>(gh + m * ir.mul + u);
+                if (gy) {
+                    q.h[k][m] = load_pack<S, V>(h + m * ir.mul + u);
+                    q.gy[k][m] = load_pack<S, V>(gy + m * ir.mul + u);
+                }
+            }
+            if (z) q.z[k] = load_pack<S, V>(z + u);
+        }
 }
 
 template <typename S, int V, int L, int K>
 __device__ __forceinline__ void backward_body(const NormIrrep& ir, int cta, const NormBackward& a,
-                                              typename Compute<S>::type (*sums)[kThreads / 32],
+                                              typename Compute<S>::type (*sums)[kMaxWarps],
                                               typename Compute<S>::type* rows) {
     using C = typename Compute<S>::type;
     constexpr int M = 2 * L + 1;
-    const int T = ir.T, t = threadIdx.x % T, G = kThreads / T;
+    const int T = ir.T, t = threadIdx.x % T, G = blockDim.x / T;
     const int U = ir.mul / V;
     const C inv_d = (C)1 / (C)(M * ir.mul), eps = (C)a.eps;
-    C w[K][V], sc[K][V], w2[K][V], acc_w[K][V], acc_s[K][V], acc_n[K][V];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = ir.ch + (t + k * T < U ? t + k * T : 0) * V;
-        load_param(w[k], (const C*)a.weight, c, (C)1);
-        load_param(sc[k], (const C*)a.scale, c, (C)1);
-        load_param(w2[k], (const C*)a.next_weight, c, (C)1);
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc_w[k][i] = acc_s[k][i] = acc_n[k][i] = 0;
-    }
-    GroupSum<C> sum{sums, T};
-    for (int64_t base = (int64_t)cta * G; base < a.n; base += (int64_t)ir.ctas * G) {
-        const int64_t row = base + threadIdx.x / T;
-        const bool in = row < a.n;
-        auto at = [&](const cgtp_rows& q) {
-            return q.data ? (const S*)q.data + row * q.stride + ir.off : nullptr;
-        };
-        const S *b = at(a.b), *h = at(a.h), *gh = at(a.grad_h), *gy = at(a.grad_y);
-        const S* z = a.gate.data ? (const S*)a.gate.data + row * a.gate.stride + ir.ch : nullptr;
-        Pack<S, V> bp[K][M], hp[K][M], gp[K][M], yp[K][M], zp[K];
+    C ws[K][V], w2[K][V], acc_a[K][V], acc_q[K][V];
+    {
+        const C* sc = (const C*)a.scale;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const bool on = in && t + k * T < U;
-            const int u = (t + k * T) * V;
+            const int c = ir.ch + (t + k * T < U ? t + k * T : 0) * V;
+            load_param(ws[k], (const C*)a.weight, c, (C)1);
+            load_param(w2[k], (const C*)a.next_weight, c, (C)1);
 #pragma unroll
-            for (int m = 0; m < M; ++m) {
-                if (on) {
-                    bp[k][m] = load_pack<S, V>(b + m * ir.mul + u);
-                    if (gh) gp[k][m] = load_pack<S, V>(gh + m * ir.mul + u);
-                    if (gy) {
-                        hp[k][m] = load_pack<S, V>(h + m * ir.mul + u);
-                        yp[k][m] = load_pack<S, V>(gy + m * ir.mul + u);
-                    }
-                }
+            for (int i = 0; i < V; ++i) {
+                ws[k][i] *= sc ? sc[c + i] : (C)1;
+                acc_a[k][i] = acc_q[k][i] = 0;
             }
-            if (on && z) zp[k] = load_pack<S, V>(z + u);
         }
+    }
+    GroupSum<C> sum{sums, T};
+    const int64_t step = (int64_t)ir.ctas * G;
+    int64_t row = (int64_t)cta * G + threadIdx.x / T;
+    constexpr bool kAhead = L == 0 && K * V * sizeof(S) <= 16;
+    BackwardRegs<S, V, L, K> q, ahead;
+    load_backward(q, ir, a, row, t);
+    for (int64_t base = (int64_t)cta * G; base < a.n; base += step, row += step) {
+        if constexpr (kAhead) load_backward(ahead, ir, a, row + step, t);
+        const bool in = row < a.n;
         C s[3] = {0, 0, 0};  // b^2, h^2, next_weight gy h
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (in && t + k * T < U)
 #pragma unroll
-                for (int m = 0; m < M; ++m)
+            for (int m = 0; m < M; ++m)
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const C v = widen(bp[k][m].v[i]);
-                        s[0] += v * v;
-                        if (gy) {
-                            const C q = widen(hp[k][m].v[i]);
-                            s[1] += q * q;
-                            s[2] += w2[k][i] * q * widen(yp[k][m].v[i]);
-                        }
-                    }
+                for (int i = 0; i < V; ++i) {
+                    const C v = q.b[k][m].get(i), x = q.h[k][m].get(i);
+                    s[0] += v * v;
+                    s[1] += x * x;
+                    s[2] += x * (w2[k][i] * q.gy[k][m].get(i));
+                }
         sum(s);
         const C r = rsqrt_of(s[0] * inv_d + eps), r2 = rsqrt_of(s[1] * inv_d + eps);
-        const C mean2 = s[2] * inv_d * r2 * r2;  // times h r': the mean's part of gx / r'
+        const C mean2 = s[2] * inv_d * r2 * r2;  // times h: the mean's part of gx / r'
         C gx[K][M][V], sig[K][V], P[K][V], dot[1] = {0};
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (in && t + k * T < U) {
+        for (int k = 0; k < K; ++k) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    sig[k][i] = z ? sigmoid_of(widen(zp[k].v[i])) : (C)1;
-                    P[k][i] = 0;
-                }
-#pragma unroll
-                for (int m = 0; m < M; ++m)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        C g = gh ? widen(gp[k][m].v[i]) : (C)0;
-                        if (gy) {
-                            const C q = widen(hp[k][m].v[i]), y = widen(yp[k][m].v[i]);
-                            g += r2 * (w2[k][i] * y - q * mean2);
-                            acc_n[k][i] += y * q * r2;
-                        }
-                        gx[k][m][i] = g;
-                        P[k][i] += g * widen(bp[k][m].v[i]);
-                    }
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    P[k][i] *= r;
-                    const C aw = sc[k][i] * sig[k][i];
-                    dot[0] += aw * w[k][i] * P[k][i];
-                    acc_w[k][i] += aw * P[k][i];
-                    acc_s[k][i] += w[k][i] * sig[k][i] * P[k][i];
-                }
+            for (int i = 0; i < V; ++i) {
+                sig[k][i] = sigmoid_of(q.z[k].get(i));
+                P[k][i] = 0;
             }
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const C x = q.h[k][m].get(i), y = q.gy[k][m].get(i);
+                    const C g = q.gh[k][m].get(i) + r2 * (w2[k][i] * y - x * mean2);
+                    acc_q[k][i] += y * (x * r2);
+                    gx[k][m][i] = g;
+                    P[k][i] += g * q.b[k][m].get(i);
+                }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                P[k][i] *= r * sig[k][i];
+                dot[0] += ws[k][i] * P[k][i];
+                acc_a[k][i] += P[k][i];
+            }
+        }
         sum(dot);
-        const C mean = dot[0] * inv_d * r;  // times b r: the mean's part of gb / r
-        auto to = [&](const cgtp_rows& q) {
-            return q.data ? (S*)q.data + row * q.stride + ir.off : nullptr;
-        };
-        S *ox = to(a.grad_x), *ob = to(a.grad_b);
-        S* oz = a.grad_gate.data ? (S*)a.grad_gate.data + row * a.grad_gate.stride + ir.ch
-                                 : nullptr;
+        const C mean = dot[0] * inv_d * r * r;  // times b: the mean's part of gb
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (in && t + k * T < U) {
                 const int u = (t + k * T) * V;
+                C f[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) f[i] = r * ws[k][i] * sig[k][i];
+                S* ox = row_of<S>(a.grad_x, row, ir.off);
+                S* ob = row_of<S>(a.grad_b, row, ir.off);
+                S* oz = row_of<S>(a.grad_gate, row, ir.ch);
 #pragma unroll
                 for (int m = 0; m < M; ++m) {
                     if (ox) {
                         Pack<S, V> p;
-#pragma unroll
-                        for (int i = 0; i < V; ++i) p.v[i] = narrow<S>(gx[k][m][i]);
+                        p.set(gx[k][m]);
                         store_pack(ox + m * ir.mul + u, p);
                     }
                     if (ob) {
+                        C v[V];
 #pragma unroll
                         for (int i = 0; i < V; ++i)
-                            bp[k][m].v[i] = narrow<S>(
-                                r * (sc[k][i] * sig[k][i] * w[k][i] * gx[k][m][i] -
-                                     widen(bp[k][m].v[i]) * mean));
-                        store_pack(ob + m * ir.mul + u, bp[k][m]);
+                            v[i] = f[i] * gx[k][m][i] - q.b[k][m].get(i) * mean;
+                        q.b[k][m].set(v);
+                        store_pack(ob + m * ir.mul + u, q.b[k][m]);
                     }
                 }
                 if (oz) {
                     Pack<S, V> p;
+                    C v[V];
 #pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        p.v[i] = narrow<S>(sc[k][i] * w[k][i] * sig[k][i] * ((C)1 - sig[k][i]) *
-                                           P[k][i]);
+                    for (int i = 0; i < V; ++i) v[i] = ws[k][i] * ((C)1 - sig[k][i]) * P[k][i];
+                    p.set(v);
                     store_pack(oz + u, p);
                 }
             }
+        if constexpr (kAhead)
+            q = ahead;
+        else
+            load_backward(q, ir, a, row + step, t);
     }
     if (!a.partial) return;
     // The groups' sums, added in group order through shared memory.
@@ -431,31 +509,30 @@ __device__ __forceinline__ void backward_body(const NormIrrep& ir, int cta, cons
 #pragma unroll
             for (int i = 0; i < V; ++i) rows[(threadIdx.x * K + k) * V + i] = acc[k][i];
         __syncthreads();
-        for (int c = threadIdx.x; c < ir.mul; c += kThreads) {
+        for (int c = threadIdx.x; c < ir.mul; c += blockDim.x) {
             const int u = c / V, k = u / T;
             C s = 0;
             for (int g = 0; g < G; ++g) s += rows[((g * T + u % T) * K + k) * V + c % V];
             out[which * ir.mul + c] = s;
         }
     };
-    flush(acc_w, 0);
-    flush(acc_s, 1);
-    flush(acc_n, 2);
+    flush(acc_a, 0);
+    flush(acc_q, 1);
 }
 
 template <typename S, int V>
 __device__ void backward_wide(const NormIrrep& ir, int cta, const NormBackward& a,
-                              typename Compute<S>::type (*sums)[kThreads / 32]) {
+                              typename Compute<S>::type (*sums)[kMaxWarps]) {
     using C = typename Compute<S>::type;
-    const int M = 2 * ir.l + 1, U = ir.mul / V;
+    const int M = 2 * ir.l + 1, U = ir.mul / V, B = blockDim.x;
     const C inv_d = (C)1 / ((C)M * (C)ir.mul), eps = (C)a.eps;
     const C *w = (const C*)a.weight, *sc = (const C*)a.scale, *w2 = (const C*)a.next_weight;
     C* part = a.partial ? partial_row<C>(ir, cta, a) : nullptr;
     if (part)  // a thread's channels are the same in every row
-        for (int u = threadIdx.x; u < U; u += kThreads)
+        for (int u = threadIdx.x; u < U; u += B)
             for (int i = 0; i < V; ++i)
-                for (int which = 0; which < 3; ++which) part[which * ir.mul + u * V + i] = 0;
-    GroupSum<C> sum{sums, kThreads};
+                for (int which = 0; which < 2; ++which) part[which * ir.mul + u * V + i] = 0;
+    GroupSum<C> sum{sums, B};
     for (int64_t row = cta; row < a.n; row += ir.ctas) {
         auto at = [&](const cgtp_rows& q) {
             return q.data ? (S*)q.data + row * q.stride + ir.off : nullptr;
@@ -466,20 +543,20 @@ __device__ void backward_wide(const NormIrrep& ir, int cta, const NormBackward& 
         S* oz = a.grad_gate.data ? (S*)a.grad_gate.data + row * a.grad_gate.stride + ir.ch
                                  : nullptr;
         C s[3] = {0, 0, 0};
-        for (int u = threadIdx.x; u < U; u += kThreads) {
+        for (int u = threadIdx.x; u < U; u += B) {
             C f[V];
             load_param(f, w2, ir.ch + u * V, (C)1);
             for (int m = 0; m < M; ++m) {
                 const int64_t e = (int64_t)m * ir.mul + (int64_t)u * V;
                 const Pack<S, V> p = load_pack<S, V>(b + e);
 #pragma unroll
-                for (int i = 0; i < V; ++i) s[0] += widen(p.v[i]) * widen(p.v[i]);
+                for (int i = 0; i < V; ++i) s[0] += p.get(i) * p.get(i);
                 if (gy) {
                     const Pack<S, V> q = load_pack<S, V>(h + e), y = load_pack<S, V>(gy + e);
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        s[1] += widen(q.v[i]) * widen(q.v[i]);
-                        s[2] += f[i] * widen(q.v[i]) * widen(y.v[i]);
+                        s[1] += q.get(i) * q.get(i);
+                        s[2] += f[i] * q.get(i) * y.get(i);
                     }
                 }
             }
@@ -490,7 +567,7 @@ __device__ void backward_wide(const NormIrrep& ir, int cta, const NormBackward& 
         // gx of element i of pack e, computed the same way in both passes
         auto grad = [&](C g, C q, C y, C f) { return gy ? g + r2 * (f * y - q * mean2) : g; };
         C dot[1] = {0};
-        for (int u = threadIdx.x; u < U; u += kThreads) {
+        for (int u = threadIdx.x; u < U; u += B) {
             const int c = ir.ch + u * V;
             C f[V], P[V], Q[V];
             load_param(f, w2, c, (C)1);
@@ -504,8 +581,8 @@ __device__ void backward_wide(const NormIrrep& ir, int cta, const NormBackward& 
                 if (gy) q = load_pack<S, V>(h + e), y = load_pack<S, V>(gy + e);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const C qv = gy ? widen(q.v[i]) : (C)0, yv = gy ? widen(y.v[i]) : (C)0;
-                    P[i] += grad(gh ? widen(g.v[i]) : (C)0, qv, yv, f[i]) * widen(p.v[i]);
+                    const C qv = gy ? q.get(i) : (C)0, yv = gy ? y.get(i) : (C)0;
+                    P[i] += grad(gh ? g.get(i) : (C)0, qv, yv, f[i]) * p.get(i);
                     Q[i] += yv * qv * r2;
                 }
             }
@@ -517,16 +594,15 @@ __device__ void backward_wide(const NormIrrep& ir, int cta, const NormBackward& 
                 dot[0] += si * sig * wi * P[i];
                 if (oz) oz[u * V + i] = narrow<S>(si * wi * sig * ((C)1 - sig) * P[i]);
                 if (part) {
-                    part[u * V + i] += si * sig * P[i];
-                    part[ir.mul + u * V + i] += wi * sig * P[i];
-                    part[2 * ir.mul + u * V + i] += Q[i];
+                    part[u * V + i] += sig * P[i];
+                    part[ir.mul + u * V + i] += Q[i];
                 }
             }
         }
         sum(dot);
         const C mean = dot[0] * inv_d * r;
         if (ox || ob)
-            for (int u = threadIdx.x; u < U; u += kThreads) {
+            for (int u = threadIdx.x; u < U; u += B) {
                 const int c = ir.ch + u * V;
                 C f[V], aw[V];
                 load_param(f, w2, c, (C)1);
@@ -540,13 +616,15 @@ __device__ void backward_wide(const NormIrrep& ir, int cta, const NormBackward& 
                     Pack<S, V> p = load_pack<S, V>(b + e), g, q, y;
                     if (gh) g = load_pack<S, V>(gh + e);
                     if (gy) q = load_pack<S, V>(h + e), y = load_pack<S, V>(gy + e);
+                    C gx[V], gb[V];
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        const C qv = gy ? widen(q.v[i]) : (C)0, yv = gy ? widen(y.v[i]) : (C)0;
-                        const C gx = grad(gh ? widen(g.v[i]) : (C)0, qv, yv, f[i]);
-                        g.v[i] = narrow<S>(gx);
-                        p.v[i] = narrow<S>(r * (aw[i] * gx - widen(p.v[i]) * mean));
+                        const C qv = gy ? q.get(i) : (C)0, yv = gy ? y.get(i) : (C)0;
+                        gx[i] = grad(gh ? g.get(i) : (C)0, qv, yv, f[i]);
+                        gb[i] = r * (aw[i] * gx[i] - p.get(i) * mean);
                     }
+                    g.set(gx);
+                    p.set(gb);
                     if (ox) store_pack(ox + e, g);
                     if (ob) store_pack(ob + e, p);
                 }
@@ -554,121 +632,448 @@ __device__ void backward_wide(const NormIrrep& ir, int cta, const NormBackward& 
     }
 }
 
-template <typename S, int V, int LC>
-__global__ void __launch_bounds__(kThreads)
+template <typename S, int V, int LC, int K>
+__global__ void __launch_bounds__(LC == 0 ? 512 : 128, LC == 3 ? 3 : 1)
 norm_backward_kernel(const __grid_constant__ NormTable tab,
                      const __grid_constant__ NormBackward a) {
     using C = typename Compute<S>::type;
-    __shared__ C sums[6][kThreads / 32];
+    __shared__ C sums[6][kMaxWarps];
     extern __shared__ __align__(16) unsigned char dynamic[];
     C* rows = reinterpret_cast<C*>(dynamic);
     int i = 0;
     while (i + 1 < tab.n && (int)blockIdx.x >= tab.ir[i + 1].cta0) ++i;
     const NormIrrep& ir = tab.ir[i];
     const int cta = blockIdx.x - ir.cta0;
-#define CALL(L, K) backward_body<S, V, L, K>(ir, cta, a, sums, rows)
-    CGTP_NORM_BODIES(LC, CALL, (backward_wide<S, V>(ir, cta, a, sums)))
+#define CALL(L, K) backward_body<S, kWidth<V, L>, L, K>(ir, cta, a, sums, rows)
+    CGTP_NORM_BODIES(LC, K, CALL, (backward_wide<S, V>(ir, cta, a, sums)))
 #undef CALL
 }
 
-// Adds the CTAs' partial rows: 32 sums a CTA, eight threads each walking every
-// eighth row, joined in order.
+// ---------------------------------------------------- long plain rows --
+
+// Rows of scalars of more than 1 KB or so (the norm of a plain residual
+// network): the CTA takes a row at a time, a thread K vectors of it.  With so
+// few elements a thread, what counts besides the bytes are the instructions a
+// row costs whatever its length: addresses, reductions, barriers.  The row
+// number is the same for the whole CTA, so its addresses are computed once a
+// warp, and the next rows arrive in shared memory by asynchronous copies, each
+// thread copying the vectors that it reads itself: no registers for rows in
+// flight and no barrier or wait on another thread.
+constexpr int kStages = 2;
+
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_end_group() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A thread's vectors of N tensors in kStages stages; tensor j's vector k of
+// stage s at ((s N + j) K + k) threads + thread, 16 bytes each.
+template <typename S, int N, int K>
+struct RowRing {
+    static constexpr int V = 16 / sizeof(S);
+    unsigned char* mine;
+    int U;
+    __device__ __forceinline__ unsigned char* slot(int s, int j, int k) const {
+        return mine + (size_t)((s * N + j) * K + k) * blockDim.x * 16;
+    }
+    __device__ __forceinline__ void fetch(int s, int j, const cgtp_rows& q, int64_t row, int at) {
+        if (!q.data) return;
+        const S* p = (const S*)q.data + row * q.stride + at;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int u = threadIdx.x + k * blockDim.x;
+            if (u < U)
+                copy_async((uint32_t)__cvta_generic_to_shared(slot(s, j, k)), p + u * V);
+        }
+    }
+    __device__ __forceinline__ Pack<S, V> get(int s, int j, int k, bool there,
+                                              typename Compute<S>::type missing) const {
+        Pack<S, V> x;
+        if (there && (int)(threadIdx.x + k * blockDim.x) < U)
+            x = *reinterpret_cast<const Pack<S, V>*>(slot(s, j, k));
+        else
+            x.fill(missing);
+        return x;
+    }
+};
+
+template <typename S, int K>
+__global__ void __launch_bounds__(256, 2)
+row_forward_kernel(const __grid_constant__ NormTable tab, const __grid_constant__ NormForward a) {
+    using C = typename Compute<S>::type;
+    constexpr int V = 16 / sizeof(S);
+    __shared__ C sums[6][kMaxWarps];
+    extern __shared__ __align__(16) unsigned char dynamic[];
+    int i = 0;
+    while (i + 1 < tab.n && (int)blockIdx.x >= tab.ir[i + 1].cta0) ++i;
+    const NormIrrep& ir = tab.ir[i];
+    const int B = blockDim.x, t = threadIdx.x, U = ir.mul / V;
+    const C inv_d = (C)1 / (C)ir.mul, eps = (C)a.eps;
+    const C *w = (const C*)a.weight, *sc = (const C*)a.scale, *w2 = (const C*)a.next_weight;
+    C coef[K][V], next[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = ir.ch + (t + k * B < U ? t + k * B : 0) * V;
+        load_param(coef[k], w, c, (C)1);
+        load_param(next[k], w2, c, (C)1);
+#pragma unroll
+        for (int j = 0; j < V; ++j) coef[k][j] *= sc ? sc[c + j] : (C)1;
+    }
+    RowRing<S, 3, K> ring{dynamic + t * 16, U};
+    auto fetch = [&](int st, int64_t row) {
+        if (row < a.n) {
+            ring.fetch(st, 0, a.b, row, ir.off);
+            ring.fetch(st, 1, a.x, row, ir.off);
+            ring.fetch(st, 2, a.gate, row, ir.ch);
+        }
+        copies_end_group();
+    };
+    GroupSum<C> sum{sums, B};
+    int64_t row = blockIdx.x - ir.cta0;
+    for (int st = 0; st < kStages; ++st) fetch(st, row + (int64_t)st * ir.ctas);
+    for (int st = 0; row < a.n; row += ir.ctas, st = st + 1 == kStages ? 0 : st + 1) {
+        copies_wait<kStages - 1>();
+        Pack<S, V> b[K];
+        C s[1] = {0};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            b[k] = ring.get(st, 0, k, true, 0);
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[0] += b[k].get(j) * b[k].get(j);
+        }
+        sum(s);
+        const C r = rsqrt_of(s[0] * inv_d + eps);
+        s[0] = 0;
+        S* h = (S*)a.h.data + row * a.h.stride + ir.off;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const Pack<S, V> x = ring.get(st, 1, k, a.x.data, 0);
+            const Pack<S, V> z = ring.get(st, 2, k, a.gate.data, INFINITY);
+            C v[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                v[j] = r * coef[k][j] * sigmoid_of(z.get(j)) * b[k].get(j) + x.get(j);
+            b[k].set(v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[0] += b[k].get(j) * b[k].get(j);
+            if (t + k * B < U) store_pack(h + (t + k * B) * V, b[k]);
+        }
+        fetch(st, row + (int64_t)kStages * ir.ctas);
+        if (a.y.data) {
+            sum(s);
+            const C r2 = rsqrt_of(s[0] * inv_d + eps);
+            S* y = (S*)a.y.data + row * a.y.stride + ir.off;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                C v[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[j] = b[k].get(j) * (r2 * next[k][j]);
+                b[k].set(v);
+                if (t + k * B < U) store_pack(y + (t + k * B) * V, b[k]);
+            }
+        }
+    }
+    copies_wait<0>();
+}
+
+template <typename S, int K>
+__global__ void __launch_bounds__(256, K * 16 / sizeof(S) > 16 ? 1 : 2)
+row_backward_kernel(const __grid_constant__ NormTable tab, const __grid_constant__ NormBackward a) {
+    using C = typename Compute<S>::type;
+    constexpr int V = 16 / sizeof(S);
+    __shared__ C sums[6][kMaxWarps];
+    extern __shared__ __align__(16) unsigned char dynamic[];
+    int i = 0;
+    while (i + 1 < tab.n && (int)blockIdx.x >= tab.ir[i + 1].cta0) ++i;
+    const NormIrrep& ir = tab.ir[i];
+    const int cta = blockIdx.x - ir.cta0, B = blockDim.x, t = threadIdx.x, U = ir.mul / V;
+    const C inv_d = (C)1 / (C)ir.mul, eps = (C)a.eps;
+    C ws[K][V], w2[K][V], acc_a[K][V], acc_q[K][V];
+    {
+        const C* sc = (const C*)a.scale;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = ir.ch + (t + k * B < U ? t + k * B : 0) * V;
+            load_param(ws[k], (const C*)a.weight, c, (C)1);
+            load_param(w2[k], (const C*)a.next_weight, c, (C)1);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                ws[k][j] *= sc ? sc[c + j] : (C)1;
+                acc_a[k][j] = acc_q[k][j] = 0;
+            }
+        }
+    }
+    RowRing<S, 5, K> ring{dynamic + t * 16, U};
+    auto fetch = [&](int st, int64_t row) {
+        if (row < a.n) {
+            ring.fetch(st, 0, a.b, row, ir.off);
+            if (a.grad_y.data) ring.fetch(st, 1, a.h, row, ir.off);
+            ring.fetch(st, 2, a.grad_y, row, ir.off);
+            ring.fetch(st, 3, a.grad_h, row, ir.off);
+            ring.fetch(st, 4, a.gate, row, ir.ch);
+        }
+        copies_end_group();
+    };
+    GroupSum<C> sum{sums, B};
+    int64_t row = cta;
+    for (int st = 0; st < kStages; ++st) fetch(st, row + (int64_t)st * ir.ctas);
+    for (int st = 0; row < a.n; row += ir.ctas, st = st + 1 == kStages ? 0 : st + 1) {
+        copies_wait<kStages - 1>();
+        Pack<S, V> b[K], h[K], y[K];
+        C s[3] = {0, 0, 0};  // b^2, h^2, next_weight gy h
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            b[k] = ring.get(st, 0, k, true, 0);
+            h[k] = ring.get(st, 1, k, a.grad_y.data, 0);
+            y[k] = ring.get(st, 2, k, a.grad_y.data, 0);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const C v = b[k].get(j), x = h[k].get(j);
+                s[0] += v * v;
+                s[1] += x * x;
+                s[2] += x * (w2[k][j] * y[k].get(j));
+            }
+        }
+        sum(s);
+        const C r = rsqrt_of(s[0] * inv_d + eps), r2 = rsqrt_of(s[1] * inv_d + eps);
+        const C mean2 = s[2] * inv_d * r2 * r2;
+        C gx[K][V], dot[1] = {0};
+        S* oz = a.grad_gate.data ? (S*)a.grad_gate.data + row * a.grad_gate.stride + ir.ch : nullptr;
+        S* ox = a.grad_x.data ? (S*)a.grad_x.data + row * a.grad_x.stride + ir.off : nullptr;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const Pack<S, V> gh = ring.get(st, 3, k, a.grad_h.data, 0);
+            const Pack<S, V> z = ring.get(st, 4, k, a.gate.data, INFINITY);
+            C f[V], v[V];
+            Pack<S, V> p;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const C x = h[k].get(j), gy = y[k].get(j), sig = sigmoid_of(z.get(j));
+                gx[k][j] = gh.get(j) + r2 * (w2[k][j] * gy - x * mean2);
+                acc_q[k][j] += gy * (x * r2);
+                const C P = gx[k][j] * b[k].get(j) * (r * sig);
+                dot[0] += ws[k][j] * P;
+                acc_a[k][j] += P;
+                v[j] = ws[k][j] * ((C)1 - sig) * P;
+                f[j] = r * ws[k][j] * sig;
+            }
+            const bool on = t + k * B < U;
+            p.set(v);
+            if (oz && on) store_pack(oz + (t + k * B) * V, p);
+            p.set(gx[k]);
+            if (ox && on) store_pack(ox + (t + k * B) * V, p);
+#pragma unroll
+            for (int j = 0; j < V; ++j) gx[k][j] *= f[j];
+        }
+        fetch(st, row + (int64_t)kStages * ir.ctas);
+        sum(dot);
+        const C mean = dot[0] * inv_d * r * r;
+        if (a.grad_b.data) {
+            S* ob = (S*)a.grad_b.data + row * a.grad_b.stride + ir.off;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                C v[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[j] = gx[k][j] - b[k].get(j) * mean;
+                b[k].set(v);
+                if (t + k * B < U) store_pack(ob + (t + k * B) * V, b[k]);
+            }
+        }
+    }
+    copies_wait<0>();
+    if (!a.partial) return;
+    C* out = partial_row<C>(ir, cta, a);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (t + k * B < U)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                out[(t + k * B) * V + j] = acc_a[k][j];
+                out[ir.mul + (t + k * B) * V + j] = acc_q[k][j];
+            }
+}
+
+// Adds the CTAs' partial rows: 32 sums a CTA, a warp for every 32nd row, joined
+// in order.
 template <typename C>
-__global__ void __launch_bounds__(256)
-norm_reduce_kernel(const __grid_constant__ NormTable tab, const C* __restrict__ partial,
-                   int channels, C* __restrict__ gw, C* __restrict__ gs, C* __restrict__ gn) {
-    __shared__ C part[8][32];
+__global__ void __launch_bounds__(1024)
+norm_reduce_kernel(const __grid_constant__ NormTable tab, const __grid_constant__ NormBackward a) {
+    __shared__ C part[32][32];
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), lane = threadIdx.x >> 5;
     const int which = blockIdx.y;
-    C* out = which == 0 ? gw : which == 1 ? gs : gn;
     C s = 0;
-    if (out && col < channels) {
+    if (col < a.channels) {
         int i = 0;
         while (i + 1 < tab.n && col >= tab.ir[i + 1].ch) ++i;
         const NormIrrep& ir = tab.ir[i];
-        const C* p = partial + ir.part0 + which * ir.mul + (col - ir.ch);
-        for (int r = lane; r < ir.ctas; r += 8) s += p[(int64_t)r * 3 * ir.mul];
+        const C* p = (const C*)a.partial + ir.part0 + which * ir.mul + (col - ir.ch);
+#pragma unroll 4
+        for (int r = lane; r < ir.ctas; r += 32) s += p[(int64_t)r * 2 * ir.mul];
     }
     part[lane][threadIdx.x & 31] = s;
     __syncthreads();
-    if (lane == 0 && out && col < channels) {
-        for (int j = 1; j < 8; ++j) s += part[j][threadIdx.x];
-        out[col] = s;
+    if (lane == 0 && col < a.channels) {
+#pragma unroll
+        for (int j = 1; j < 32; ++j) s += part[j][threadIdx.x];
+        if (which == 0) {
+            const C *w = (const C*)a.weight, *sc = (const C*)a.scale;
+            if (a.grad_weight) ((C*)a.grad_weight)[col] = sc ? s * sc[col] : s;
+            if (a.grad_scale) ((C*)a.grad_scale)[col] = w ? s * w[col] : s;
+        } else if (a.grad_next_weight) {
+            ((C*)a.grad_next_weight)[col] = s;
+        }
     }
 }
 
 // ------------------------------------------------------------ launching --
 
-// T, K and the CTAs of each irrep for vectors of V channels.
-template <typename S>
-void shape_table(NormTable& tab, int V, int64_t n) {
-    int cta0 = 0;
+// T, K and the CTAs of each irrep; returns the threads of a CTA: `threads`, with
+// rows of up to that many vectors.  Plain rows may have 512 threads with up to
+// four vectors each (two of eight 16-bit channels).
+template <int V>
+int shape_table(NormTable& tab, int64_t n, int threads, int& most_k, int& most_l) {
+    most_l = 0;
+    for (int i = 0; i < tab.n; ++i) most_l = std::max(most_l, tab.ir[i].l);
+    most_k = 1;
+    const int most_t = most_l == 0 ? 512 : threads;
+    if (most_l == 0) threads = 256;
     for (int i = 0; i < tab.n; ++i) {
         NormIrrep& ir = tab.ir[i];
-        const int U = ir.mul / V;
-        int T = 1;
-        while (T < U && T < kThreads) T *= 2;
-        const int most = ir.l == 0 ? 8 : ir.l == 1 ? 2 : 1;
-        int K = 1;
-        while (K * T < U && K <= most) K *= 2;
-        if (K > most) K = 0, T = kThreads;  // the body that reads again
-        ir.T = T;
-        ir.K = K;
-        const int64_t G = kThreads / T;
+        const int U = ir.mul / (V == 8 && ir.l > 1 ? 4 : V);
+        ir.T = 1;
+        ir.K = 1;
+        while (ir.T < U && ir.T < most_t) ir.T *= 2;
+        while (ir.K * ir.T < U) ir.K *= 2;
+        if (ir.K > (most_l > 0 ? 1 : V == 8 ? 2 : 4)) ir.K = 0;  // the body that reads again
+        most_k = std::max(most_k, ir.K);
+        threads = std::max(threads, ir.T);
+    }
+    tab.ctas = 0;
+    for (int i = 0; i < tab.n; ++i) {
+        NormIrrep& ir = tab.ir[i];
+        if (ir.K == 0) ir.T = threads;
+        const int64_t G = threads / ir.T;
         ir.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(ir.max_ctas, (n + G - 1) / G));
-        ir.cta0 = cta0;
-        cta0 += ir.ctas;
+        ir.cta0 = tab.ctas;
+        tab.ctas += ir.ctas;
     }
-    tab.ctas = cta0;
+    return threads;
 }
 
-template <typename S, int V, int LC>
-cudaError_t forward_v(const NormTable& tab, const NormForward& a, cudaStream_t s) {
-    norm_forward_kernel<S, V, LC><<<tab.ctas, kThreads, 0, s>>>(tab, a);
+template <typename C>
+cudaError_t finish(const NormTable&, const NormForward&, cudaStream_t) {
+    return cudaSuccess;
+}
+template <typename C>
+cudaError_t finish(const NormTable& tab, const NormBackward& a, cudaStream_t s) {
+    if (!a.partial) return cudaSuccess;
+    norm_reduce_kernel<C><<<dim3((unsigned)((a.channels + 31) / 32), 2), 1024, 0, s>>>(tab, a);
     count_launch();
     return cudaGetLastError();
 }
 
-template <typename S, int V, int LC>
-cudaError_t backward_v(const NormTable& tab, const NormBackward& a, cudaStream_t s) {
+template <typename S, int V, int LC, int K>
+cudaError_t launch(const NormTable& tab, int threads, const NormForward& a, cudaStream_t s) {
+    norm_forward_kernel<S, V, LC, K><<<tab.ctas, threads, 0, s>>>(tab, a);
+    count_launch();
+    return cudaGetLastError();
+}
+
+template <typename S, int V, int LC, int K>
+cudaError_t launch(const NormTable& tab, int threads, const NormBackward& a, cudaStream_t s) {
     using C = typename Compute<S>::type;
-    size_t smem = 0;  // one set of channel sums of every thread
-    for (int i = 0; i < tab.n; ++i)
-        smem = std::max(smem, (size_t)kThreads * std::max(1, tab.ir[i].K) * V * sizeof(C));
-    if (!a.partial) smem = 0;
-    cudaError_t e = cudaFuncSetAttribute(norm_backward_kernel<S, V, LC>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kThreads * 8 * V * (int)sizeof(C));
-    if (e != cudaSuccess) return e;
-    norm_backward_kernel<S, V, LC><<<tab.ctas, kThreads, smem, s>>>(tab, a);
+    // one set of channel sums of every thread
+    const int smem = a.partial ? threads * K * V * (int)sizeof(C) : 0;
+    if (smem > 48 << 10) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            norm_backward_kernel<S, V, LC, K>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    norm_backward_kernel<S, V, LC, K><<<tab.ctas, threads, smem, s>>>(tab, a);
     count_launch();
-    e = cudaGetLastError();
-    if (e != cudaSuccess || !a.partial) return e;
-    const dim3 grid((unsigned)((a.channels + 31) / 32), 3);
-    norm_reduce_kernel<C><<<grid, 256, 0, s>>>(tab, (const C*)a.partial, a.channels,
-                                               (C*)a.grad_weight, (C*)a.grad_scale,
-                                               (C*)a.grad_next_weight);
-    count_launch();
-    return cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : finish<C>(tab, a, s);
 }
 
-#define CGTP_NORM_LAUNCH(NAME, ARGS)                                            \
-    template <typename S>                                                       \
-    cudaError_t NAME(NormTable tab, const ARGS& a, bool vectors, cudaStream_t s) { \
-        constexpr int W = sizeof(S) == 8 ? 2 : 4;                               \
-        shape_table<S>(tab, vectors ? W : 1, a.n);                              \
-        int l = 0;                                                              \
-        for (int i = 0; i < tab.n; ++i) l = std::max(l, tab.ir[i].l);           \
-        if (vectors)                                                            \
-            return l == 0   ? NAME##_v<S, W, 0>(tab, a, s)                      \
-                   : l <= 3 ? NAME##_v<S, W, 3>(tab, a, s)                      \
-                            : NAME##_v<S, W, 6>(tab, a, s);                     \
-        return l == 0   ? NAME##_v<S, 1, 0>(tab, a, s)                          \
-               : l <= 3 ? NAME##_v<S, 1, 3>(tab, a, s)                          \
-                        : NAME##_v<S, 1, 6>(tab, a, s);                         \
+template <typename S, int K>
+const void* row_kernel(const NormForward&) {
+    return (const void*)row_forward_kernel<S, K>;
+}
+template <typename S, int K>
+const void* row_kernel(const NormBackward&) {
+    return (const void*)row_backward_kernel<S, K>;
+}
+template <typename S, int K, typename Args>
+cudaError_t launch_rows(const NormTable& tab, int threads, const Args& a, cudaStream_t s) {
+    const void* f = row_kernel<S, K>(a);
+    const size_t smem = (size_t)kStages * Args::kInputs * K * threads * 16;
+    cudaError_t e =
+        cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    void* args[] = {const_cast<NormTable*>(&tab), const_cast<Args*>(&a)};
+    e = cudaLaunchKernel(f, dim3(tab.ctas), dim3(threads), args, smem, s);
+    count_launch();
+    if (e != cudaSuccess) return e;
+    return finish<typename Compute<S>::type>(tab, a, s);
+}
+
+// Rows of scalars only, of 64 to 1024 vectors of 16 bytes.
+template <typename S, typename Args>
+bool rows_apply(NormTable& tab, int64_t n, int& threads, int& K) {
+    constexpr int V = 16 / sizeof(S);
+    int most = 0;
+    for (int i = 0; i < tab.n; ++i) {
+        if (tab.ir[i].l != 0) return false;
+        most = std::max(most, tab.ir[i].mul / V);
     }
-CGTP_NORM_LAUNCH(forward, NormForward)
-CGTP_NORM_LAUNCH(backward, NormBackward)
+    if (most < 64 || most > 1024) return false;
+    K = most > 512 ? 4 : 2;
+    threads = 32;
+    while (threads * K < most) threads *= 2;
+    tab.ctas = 0;
+    for (int i = 0; i < tab.n; ++i) {
+        NormIrrep& ir = tab.ir[i];
+        ir.K = K;
+        ir.T = threads;
+        ir.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(ir.max_ctas, n));
+        ir.cta0 = tab.ctas;
+        tab.ctas += ir.ctas;
+    }
+    return true;
+}
+
+template <typename S, int V, typename Args>
+cudaError_t launch_v(NormTable tab, const Args& a, cudaStream_t s) {
+    int k, l;
+    if constexpr (V * sizeof(S) == 16) {
+        int threads;
+        if (rows_apply<S, Args>(tab, a.n, threads, k))
+            return k == 2 ? launch_rows<S, 2>(tab, threads, a, s)
+                          : launch_rows<S, 4>(tab, threads, a, s);
+    }
+    const int threads = shape_table<V>(tab, a.n, Args::kThreads, k, l);
+    if (l > 3) return launch<S, V, 6, 1>(tab, threads, a, s);
+    if (l > 0) return launch<S, V, 3, 1>(tab, threads, a, s);
+    if (k == 1) return launch<S, V, 0, 1>(tab, threads, a, s);
+    if constexpr (V < 8)
+        if (k == 4) return launch<S, V, 0, 4>(tab, threads, a, s);
+    return launch<S, V, 0, 2>(tab, threads, a, s);
+}
+
+template <typename S, typename Args>
+cudaError_t launch_norm(const NormTable& tab, const Args& a, int vector, cudaStream_t s) {
+    if constexpr (sizeof(S) == 8)
+        return vector >= 2 ? launch_v<S, 2>(tab, a, s) : launch_v<S, 1>(tab, a, s);
+    if constexpr (sizeof(S) == 2)
+        if (vector == 8) return launch_v<S, 8>(tab, a, s);
+    return vector >= 4 ? launch_v<S, 4>(tab, a, s) : launch_v<S, 1>(tab, a, s);
+}
 
 }  // namespace
 

@@ -79,7 +79,7 @@ static bool irrep_tables(cgtp_norm_s& h, const std::vector<Irrep>& irreps) {
         h.forward.ir[i] = e;
         e.max_ctas = (int)std::max<int64_t>(1, kNormBackwardCtas * width / h.dim);
         e.part0 = part;
-        part += (int64_t)e.max_ctas * 3 * ir.mul;
+        part += (int64_t)e.max_ctas * 2 * ir.mul;
         h.backward.ir[i] = e;
         off += width;
         ch += ir.mul;
@@ -115,18 +115,20 @@ static cgtp_status norm_check(cgtp_norm h, int64_t n, std::initializer_list<cons
     return CGTP_OK;
 }
 
-// 16-byte accesses (8-byte ones for 16-bit rows) everywhere.
-static bool norm_vectors(const cgtp_norm_s& h, std::initializer_list<cgtp_rows> rows) {
-    const int V = h.dtype == CGTP_F64 ? 2 : 4;
-    for (int i = 0; i < h.forward.n; ++i)
-        if (h.forward.ir[i].mul % V) return false;
-    for (const cgtp_rows& r : rows)
-        if (r.data && (!on(r.data, V * size_of(h.dtype)) || r.stride % V)) return false;
-    return true;
+// The widest access that every multiplicity, address and stride allows.
+static int norm_vector(const cgtp_norm_s& h, std::initializer_list<cgtp_rows> rows) {
+    for (int V = h.dtype == CGTP_F64 ? 2 : h.dtype == CGTP_F32 ? 4 : 8; V > 1; V /= 2) {
+        bool ok = true;
+        for (int i = 0; i < h.forward.n; ++i) ok = ok && h.forward.ir[i].mul % V == 0;
+        for (const cgtp_rows& r : rows)
+            if (r.data) ok = ok && on(r.data, V * size_of(h.dtype)) && r.stride % V == 0;
+        if (ok) return V;
+    }
+    return 1;
 }
 
 static cudaError_t run_forward(const cgtp_norm_s& h, const NormForward& a, cudaStream_t s) {
-    const bool v = norm_vectors(h, {a.b, a.x, a.gate, a.h, a.y});
+    const int v = norm_vector(h, {a.b, a.x, a.gate, a.h, a.y});
     switch (h.dtype) {
         case CGTP_F64: return launch_norm_forward_f64(h.forward, a, v, s);
         case CGTP_BF16: return launch_norm_forward_bf16(h.forward, a, v, s);
@@ -136,7 +138,7 @@ static cudaError_t run_forward(const cgtp_norm_s& h, const NormForward& a, cudaS
 }
 
 static cudaError_t run_backward(const cgtp_norm_s& h, const NormBackward& a, cudaStream_t s) {
-    const bool v = norm_vectors(
+    const int v = norm_vector(
         h, {a.b, a.h, a.gate, a.grad_h, a.grad_y, a.grad_x, a.grad_b, a.grad_gate});
     switch (h.dtype) {
         case CGTP_F64: return launch_norm_backward_f64(h.backward, a, v, s);
