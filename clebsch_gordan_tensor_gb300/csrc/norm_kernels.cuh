@@ -42,6 +42,11 @@ constexpr int kMaxWarps = 16;
 // in registers.
 template <int V, int L>
 constexpr int kWidth = V == 8 && L > 1 ? 4 : V;
+// Vectors of a thread for degree l > 0.  Single elements (rows or
+// multiplicities that no wider access fits) come several to a thread, so that a
+// pair still fits a few warps and has as much in flight.
+template <int V, int L>
+constexpr int kEach = V > 1 ? 1 : L <= 3 ? 4 : 2;
 
 __device__ __forceinline__ float rsqrt_of(float x) { return rsqrtf(x); }
 __device__ __forceinline__ double rsqrt_of(double x) { return 1.0 / sqrt(x); }
@@ -292,27 +297,26 @@ __device__ void forward_wide(const NormIrrep& ir, int cta, const NormForward& a,
 }
 
 // LC: the largest l a launch holds, in classes (0, 3 or 6), so that plain rows
-// do not carry the registers of 13 components; K: vectors of a thread, above 1
-// for plain rows only.
-#define CGTP_NORM_BODIES(LC, K, CALL, WIDE)     \
-    if (ir.K == 0) {                            \
-        WIDE;                                   \
-    } else if (ir.l == 0) {                     \
-        CALL(0, K);                             \
-    }                                           \
-    if constexpr (LC >= 3) {                    \
-        if (ir.K != 0) {                        \
-            if (ir.l == 1) CALL(1, 1);          \
-            if (ir.l == 2) CALL(2, 1);          \
-            if (ir.l == 3) CALL(3, 1);          \
-        }                                       \
-    }                                           \
-    if constexpr (LC >= 6) {                    \
-        if (ir.K != 0) {                        \
-            if (ir.l == 4) CALL(4, 1);          \
-            if (ir.l == 5) CALL(5, 1);          \
-            if (ir.l == 6) CALL(6, 1);          \
-        }                                       \
+// do not carry the registers of 13 components; K: vectors of a thread in them.
+#define CGTP_NORM_BODIES(LC, V, K, CALL, WIDE)           \
+    if (ir.K == 0) {                                     \
+        WIDE;                                            \
+    } else if (ir.l == 0) {                              \
+        CALL(0, K);                                      \
+    }                                                    \
+    if constexpr (LC >= 3) {                             \
+        if (ir.K != 0) {                                 \
+            if (ir.l == 1) CALL(1, (kEach<V, 1>));       \
+            if (ir.l == 2) CALL(2, (kEach<V, 2>));       \
+            if (ir.l == 3) CALL(3, (kEach<V, 3>));       \
+        }                                                \
+    }                                                    \
+    if constexpr (LC >= 6) {                             \
+        if (ir.K != 0) {                                 \
+            if (ir.l == 4) CALL(4, (kEach<V, 4>));       \
+            if (ir.l == 5) CALL(5, (kEach<V, 5>));       \
+            if (ir.l == 6) CALL(6, (kEach<V, 6>));       \
+        }                                                \
     }
 
 // Plain rows: 512 threads with 64 registers, two CTAs an SM (128 and one CTA
@@ -329,7 +333,7 @@ norm_forward_kernel(const __grid_constant__ NormTable tab, const __grid_constant
     const NormIrrep& ir = tab.ir[i];
     const int cta = blockIdx.x - ir.cta0;
 #define CALL(L, K) forward_body<S, kWidth<V, L>, L, K>(ir, cta, a, sums)
-    CGTP_NORM_BODIES(LC, K, CALL, (forward_wide<S, V>(ir, cta, a, sums)))
+    CGTP_NORM_BODIES(LC, V, K, CALL, (forward_wide<S, V>(ir, cta, a, sums)))
 #undef CALL
 }
 
@@ -645,7 +649,7 @@ norm_backward_kernel(const __grid_constant__ NormTable tab,
     const NormIrrep& ir = tab.ir[i];
     const int cta = blockIdx.x - ir.cta0;
 #define CALL(L, K) backward_body<S, kWidth<V, L>, L, K>(ir, cta, a, sums, rows)
-    CGTP_NORM_BODIES(LC, K, CALL, (backward_wide<S, V>(ir, cta, a, sums)))
+    CGTP_NORM_BODIES(LC, V, K, CALL, (backward_wide<S, V>(ir, cta, a, sums)))
 #undef CALL
 }
 
@@ -682,6 +686,15 @@ struct RowRing {
     __device__ __forceinline__ unsigned char* slot(int s, int j, int k) const {
         return mine + (size_t)((s * N + j) * K + k) * blockDim.x * 16;
     }
+    // Absent tensors and the threads past the row's end keep these values.
+    __device__ __forceinline__ void fill(int j, typename Compute<S>::type missing) {
+        Pack<S, V> x;
+        x.fill(missing);
+#pragma unroll
+        for (int s = 0; s < kStages; ++s)
+#pragma unroll
+            for (int k = 0; k < K; ++k) *reinterpret_cast<Pack<S, V>*>(slot(s, j, k)) = x;
+    }
     __device__ __forceinline__ void fetch(int s, int j, const cgtp_rows& q, int64_t row, int at) {
         if (!q.data) return;
         const S* p = (const S*)q.data + row * q.stride + at;
@@ -692,14 +705,65 @@ struct RowRing {
                 copy_async((uint32_t)__cvta_generic_to_shared(slot(s, j, k)), p + u * V);
         }
     }
-    __device__ __forceinline__ Pack<S, V> get(int s, int j, int k, bool there,
-                                              typename Compute<S>::type missing) const {
-        Pack<S, V> x;
-        if (there && (int)(threadIdx.x + k * blockDim.x) < U)
-            x = *reinterpret_cast<const Pack<S, V>*>(slot(s, j, k));
-        else
-            x.fill(missing);
-        return x;
+    __device__ __forceinline__ Pack<S, V> get(int s, int j, int k) const {
+        return *reinterpret_cast<const Pack<S, V>*>(slot(s, j, k));
+    }
+};
+
+template <typename C>
+__device__ __forceinline__ Two<C> sigmoid_of(Two<C> z) {
+    return {sigmoid_of(z.x), sigmoid_of(z.y)};
+}
+template <typename C, int H>
+__device__ __forceinline__ void load_twos(Two<C> (&out)[H], const C* p, int at) {
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+        out[i] = p ? Two<C>{p[at + 2 * i], p[at + 2 * i + 1]} : Two<C>{(C)1, (C)1};
+}
+
+// Sums over a CTA of up to eight warps for the row kernels: R values, 1 or 3.
+// A warp's lanes share the work of three values (6 shuffles, not 15), and after
+// the barrier every thread adds the warps' sums from vector loads, so that no
+// further shuffle is on the path.  Two sets of slots in turn, as GroupSum.
+template <typename C>
+struct RowSum {
+    C (*buf)[8];  // [2][3][8], zero past the CTA's warps
+    int flip = 0;
+    __device__ __forceinline__ C* side() {
+        C* p = &buf[3 * flip][0];
+        flip ^= 1;
+        return p;
+    }
+    static __device__ __forceinline__ C total(const C* p) {
+        C x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = p[i];
+        return ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+    }
+    __device__ __forceinline__ void operator()(C (&v)[1]) {
+        C* p = side();
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+        if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = v[0];
+        __syncthreads();
+        v[0] = total(p);
+    }
+    __device__ __forceinline__ void operator()(C (&v)[3]) {
+        C* p = side();
+        const int lane = threadIdx.x & 31;
+        // the lower half keeps values 0 and 1, the upper half 2 and a zero
+        const bool up = lane & 16;
+        C x = up ? v[2] : v[0], y = up ? (C)0 : v[1];
+        x += __shfl_xor_sync(0xFFFFFFFFu, up ? v[0] : v[2], 16);
+        y += __shfl_xor_sync(0xFFFFFFFFu, up ? v[1] : (C)0, 16);
+        const bool odd = lane & 8;  // then one value a lane: 0, 1, 2 or none
+        C z = (odd ? y : x) + __shfl_xor_sync(0xFFFFFFFFu, odd ? x : y, 8);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+        if ((lane & 7) == 0 && lane < 24) p[(lane >> 3) * 8 + (threadIdx.x >> 5)] = z;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 3; ++r) v[r] = total(p + 8 * r);
     }
 };
 
@@ -707,25 +771,32 @@ template <typename S, int K>
 __global__ void __launch_bounds__(256, 2)
 row_forward_kernel(const __grid_constant__ NormTable tab, const __grid_constant__ NormForward a) {
     using C = typename Compute<S>::type;
-    constexpr int V = 16 / sizeof(S);
-    __shared__ C sums[6][kMaxWarps];
+    constexpr int V = 16 / sizeof(S), H = V / 2;
+    __shared__ __align__(16) C sums[6][8];
+    if (threadIdx.x < 48) (&sums[0][0])[threadIdx.x] = 0;
+    if (blockDim.x < 64 && threadIdx.x < 16) (&sums[4][0])[threadIdx.x] = 0;
+    __syncthreads();
     extern __shared__ __align__(16) unsigned char dynamic[];
     int i = 0;
     while (i + 1 < tab.n && (int)blockIdx.x >= tab.ir[i + 1].cta0) ++i;
     const NormIrrep& ir = tab.ir[i];
     const int B = blockDim.x, t = threadIdx.x, U = ir.mul / V;
     const C inv_d = (C)1 / (C)ir.mul, eps = (C)a.eps;
-    const C *w = (const C*)a.weight, *sc = (const C*)a.scale, *w2 = (const C*)a.next_weight;
-    C coef[K][V], next[K][V];
+    Two<C> coef[K][H], next[K][H];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int c = ir.ch + (t + k * B < U ? t + k * B : 0) * V;
-        load_param(coef[k], w, c, (C)1);
-        load_param(next[k], w2, c, (C)1);
+        Two<C> sc[H];
+        load_twos(coef[k], (const C*)a.weight, c);
+        load_twos(sc, (const C*)a.scale, c);
+        load_twos(next[k], (const C*)a.next_weight, c);
 #pragma unroll
-        for (int j = 0; j < V; ++j) coef[k][j] *= sc ? sc[c + j] : (C)1;
+        for (int j = 0; j < H; ++j) coef[k][j] = coef[k][j] * sc[j];
     }
     RowRing<S, 3, K> ring{dynamic + t * 16, U};
+    ring.fill(0, 0);
+    ring.fill(1, 0);
+    ring.fill(2, INFINITY);
     auto fetch = [&](int st, int64_t row) {
         if (row < a.n) {
             ring.fetch(st, 0, a.b, row, ir.off);
@@ -734,47 +805,52 @@ row_forward_kernel(const __grid_constant__ NormTable tab, const __grid_constant_
         }
         copies_end_group();
     };
-    GroupSum<C> sum{sums, B};
+    RowSum<C> sum{sums};
     int64_t row = blockIdx.x - ir.cta0;
     for (int st = 0; st < kStages; ++st) fetch(st, row + (int64_t)st * ir.ctas);
     for (int st = 0; row < a.n; row += ir.ctas, st = st + 1 == kStages ? 0 : st + 1) {
         copies_wait<kStages - 1>();
         Pack<S, V> b[K];
-        C s[1] = {0};
+        Two<C> part{0, 0};
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            b[k] = ring.get(st, 0, k, true, 0);
+            b[k] = ring.get(st, 0, k);
 #pragma unroll
-            for (int j = 0; j < V; ++j) s[0] += b[k].get(j) * b[k].get(j);
+            for (int j = 0; j < H; ++j) part = fma(two_at(b[k], j), two_at(b[k], j), part);
         }
+        C s[1] = {part.x + part.y};
         sum(s);
         const C r = rsqrt_of(s[0] * inv_d + eps);
-        s[0] = 0;
+        const Two<C> rr{r, r};
+        part = {0, 0};
         S* h = (S*)a.h.data + row * a.h.stride + ir.off;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const Pack<S, V> x = ring.get(st, 1, k, a.x.data, 0);
-            const Pack<S, V> z = ring.get(st, 2, k, a.gate.data, INFINITY);
-            C v[V];
+            const Pack<S, V> x = ring.get(st, 1, k);
+            const Pack<S, V> z = ring.get(st, 2, k);
+            Two<C> v[H];
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                v[j] = r * coef[k][j] * sigmoid_of(z.get(j)) * b[k].get(j) + x.get(j);
-            b[k].set(v);
+            for (int j = 0; j < H; ++j)
+                v[j] = fma(rr * coef[k][j] * sigmoid_of(two_at(z, j)), two_at(b[k], j),
+                           two_at(x, j));
+            set_twos(b[k], v);
 #pragma unroll
-            for (int j = 0; j < V; ++j) s[0] += b[k].get(j) * b[k].get(j);
+            for (int j = 0; j < H; ++j) part = fma(two_at(b[k], j), two_at(b[k], j), part);
             if (t + k * B < U) store_pack(h + (t + k * B) * V, b[k]);
         }
         fetch(st, row + (int64_t)kStages * ir.ctas);
         if (a.y.data) {
+            s[0] = part.x + part.y;
             sum(s);
             const C r2 = rsqrt_of(s[0] * inv_d + eps);
             S* y = (S*)a.y.data + row * a.y.stride + ir.off;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                C v[V];
+                Two<C> v[H];
 #pragma unroll
-                for (int j = 0; j < V; ++j) v[j] = b[k].get(j) * (r2 * next[k][j]);
-                b[k].set(v);
+                for (int j = 0; j < H; ++j)
+                    v[j] = two_at(b[k], j) * (Two<C>{r2, r2} * next[k][j]);
+                set_twos(b[k], v);
                 if (t + k * B < U) store_pack(y + (t + k * B) * V, b[k]);
             }
         }
@@ -786,30 +862,34 @@ template <typename S, int K>
 __global__ void __launch_bounds__(256, K * 16 / sizeof(S) > 16 ? 1 : 2)
 row_backward_kernel(const __grid_constant__ NormTable tab, const __grid_constant__ NormBackward a) {
     using C = typename Compute<S>::type;
-    constexpr int V = 16 / sizeof(S);
-    __shared__ C sums[6][kMaxWarps];
+    constexpr int V = 16 / sizeof(S), H = V / 2;
+    __shared__ __align__(16) C sums[6][8];
+    if (threadIdx.x < 48) (&sums[0][0])[threadIdx.x] = 0;
+    if (blockDim.x < 64 && threadIdx.x < 16) (&sums[4][0])[threadIdx.x] = 0;
+    __syncthreads();
     extern __shared__ __align__(16) unsigned char dynamic[];
     int i = 0;
     while (i + 1 < tab.n && (int)blockIdx.x >= tab.ir[i + 1].cta0) ++i;
     const NormIrrep& ir = tab.ir[i];
     const int cta = blockIdx.x - ir.cta0, B = blockDim.x, t = threadIdx.x, U = ir.mul / V;
     const C inv_d = (C)1 / (C)ir.mul, eps = (C)a.eps;
-    C ws[K][V], w2[K][V], acc_a[K][V], acc_q[K][V];
-    {
-        const C* sc = (const C*)a.scale;
+    Two<C> ws[K][H], w2[K][H], acc_a[K][H], acc_q[K][H];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = ir.ch + (t + k * B < U ? t + k * B : 0) * V;
-            load_param(ws[k], (const C*)a.weight, c, (C)1);
-            load_param(w2[k], (const C*)a.next_weight, c, (C)1);
+    for (int k = 0; k < K; ++k) {
+        const int c = ir.ch + (t + k * B < U ? t + k * B : 0) * V;
+        Two<C> sc[H];
+        load_twos(ws[k], (const C*)a.weight, c);
+        load_twos(sc, (const C*)a.scale, c);
+        load_twos(w2[k], (const C*)a.next_weight, c);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                ws[k][j] *= sc ? sc[c + j] : (C)1;
-                acc_a[k][j] = acc_q[k][j] = 0;
-            }
+        for (int j = 0; j < H; ++j) {
+            ws[k][j] = ws[k][j] * sc[j];
+            acc_a[k][j] = acc_q[k][j] = {0, 0};
         }
     }
     RowRing<S, 5, K> ring{dynamic + t * 16, U};
+    for (int j = 0; j < 4; ++j) ring.fill(j, 0);
+    ring.fill(4, INFINITY);
     auto fetch = [&](int st, int64_t row) {
         if (row < a.n) {
             ring.fetch(st, 0, a.b, row, ir.off);
@@ -820,68 +900,75 @@ row_backward_kernel(const __grid_constant__ NormTable tab, const __grid_constant
         }
         copies_end_group();
     };
-    GroupSum<C> sum{sums, B};
+    RowSum<C> sum{sums};
     int64_t row = cta;
     for (int st = 0; st < kStages; ++st) fetch(st, row + (int64_t)st * ir.ctas);
     for (int st = 0; row < a.n; row += ir.ctas, st = st + 1 == kStages ? 0 : st + 1) {
         copies_wait<kStages - 1>();
         Pack<S, V> b[K], h[K], y[K];
-        C s[3] = {0, 0, 0};  // b^2, h^2, next_weight gy h
+        Two<C> p0{0, 0}, p1{0, 0}, p2{0, 0};  // b^2, h^2, next_weight gy h
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            b[k] = ring.get(st, 0, k, true, 0);
-            h[k] = ring.get(st, 1, k, a.grad_y.data, 0);
-            y[k] = ring.get(st, 2, k, a.grad_y.data, 0);
+            b[k] = ring.get(st, 0, k);
+            h[k] = ring.get(st, 1, k);
+            y[k] = ring.get(st, 2, k);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const C v = b[k].get(j), x = h[k].get(j);
-                s[0] += v * v;
-                s[1] += x * x;
-                s[2] += x * (w2[k][j] * y[k].get(j));
+            for (int j = 0; j < H; ++j) {
+                const Two<C> v = two_at(b[k], j), x = two_at(h[k], j);
+                p0 = fma(v, v, p0);
+                p1 = fma(x, x, p1);
+                p2 = fma(x, w2[k][j] * two_at(y[k], j), p2);
             }
         }
+        C s[3] = {p0.x + p0.y, p1.x + p1.y, p2.x + p2.y};
         sum(s);
         const C r = rsqrt_of(s[0] * inv_d + eps), r2 = rsqrt_of(s[1] * inv_d + eps);
-        const C mean2 = s[2] * inv_d * r2 * r2;
-        C gx[K][V], dot[1] = {0};
+        const C mean2 = -s[2] * inv_d * r2 * r2;
+        const Two<C> rr{r, r}, rr2{r2, r2}, mm2{mean2, mean2};
+        Two<C> gx[K][H], dot{0, 0};
         S* oz = a.grad_gate.data ? (S*)a.grad_gate.data + row * a.grad_gate.stride + ir.ch : nullptr;
         S* ox = a.grad_x.data ? (S*)a.grad_x.data + row * a.grad_x.stride + ir.off : nullptr;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const Pack<S, V> gh = ring.get(st, 3, k, a.grad_h.data, 0);
-            const Pack<S, V> z = ring.get(st, 4, k, a.gate.data, INFINITY);
-            C f[V], v[V];
+            const Pack<S, V> gh = ring.get(st, 3, k);
+            const Pack<S, V> z = ring.get(st, 4, k);
+            Two<C> f[H], v[H];
             Pack<S, V> p;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const C x = h[k].get(j), gy = y[k].get(j), sig = sigmoid_of(z.get(j));
-                gx[k][j] = gh.get(j) + r2 * (w2[k][j] * gy - x * mean2);
-                acc_q[k][j] += gy * (x * r2);
-                const C P = gx[k][j] * b[k].get(j) * (r * sig);
-                dot[0] += ws[k][j] * P;
-                acc_a[k][j] += P;
-                v[j] = ws[k][j] * ((C)1 - sig) * P;
-                f[j] = r * ws[k][j] * sig;
+            for (int j = 0; j < H; ++j) {
+                const Two<C> x = two_at(h[k], j), gy = two_at(y[k], j);
+                const Two<C> sig = sigmoid_of(two_at(z, j));
+                gx[k][j] = fma(rr2, fma(x, mm2, w2[k][j] * gy), two_at(gh, j));
+                acc_q[k][j] = fma(gy, x * rr2, acc_q[k][j]);
+                const Two<C> rs = rr * sig;
+                const Two<C> P = gx[k][j] * two_at(b[k], j) * rs;
+                acc_a[k][j] = acc_a[k][j] + P;
+                const Two<C> wp = ws[k][j] * P;
+                dot = dot + wp;
+                v[j] = wp * fma(sig, Two<C>{-1, -1}, Two<C>{1, 1});
+                f[j] = ws[k][j] * rs;
             }
             const bool on = t + k * B < U;
-            p.set(v);
+            set_twos(p, v);
             if (oz && on) store_pack(oz + (t + k * B) * V, p);
-            p.set(gx[k]);
+            set_twos(p, gx[k]);
             if (ox && on) store_pack(ox + (t + k * B) * V, p);
 #pragma unroll
-            for (int j = 0; j < V; ++j) gx[k][j] *= f[j];
+            for (int j = 0; j < H; ++j) gx[k][j] = gx[k][j] * f[j];
         }
         fetch(st, row + (int64_t)kStages * ir.ctas);
-        sum(dot);
-        const C mean = dot[0] * inv_d * r * r;
+        C d[1] = {dot.x + dot.y};
+        sum(d);
+        const C mean = -d[0] * inv_d * r * r;
         if (a.grad_b.data) {
             S* ob = (S*)a.grad_b.data + row * a.grad_b.stride + ir.off;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                C v[V];
+                Two<C> v[H];
 #pragma unroll
-                for (int j = 0; j < V; ++j) v[j] = gx[k][j] - b[k].get(j) * mean;
-                b[k].set(v);
+                for (int j = 0; j < H; ++j)
+                    v[j] = fma(two_at(b[k], j), Two<C>{mean, mean}, gx[k][j]);
+                set_twos(b[k], v);
                 if (t + k * B < U) store_pack(ob + (t + k * B) * V, b[k]);
             }
         }
@@ -893,9 +980,10 @@ row_backward_kernel(const __grid_constant__ NormTable tab, const __grid_constant
     for (int k = 0; k < K; ++k)
         if (t + k * B < U)
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                out[(t + k * B) * V + j] = acc_a[k][j];
-                out[ir.mul + (t + k * B) * V + j] = acc_q[k][j];
+            for (int j = 0; j < H; ++j) {
+                C* o = out + (t + k * B) * V + 2 * j;
+                o[0] = acc_a[k][j].x, o[1] = acc_a[k][j].y;
+                o[ir.mul] = acc_q[k][j].x, o[ir.mul + 1] = acc_q[k][j].y;
             }
 }
 
@@ -935,23 +1023,25 @@ norm_reduce_kernel(const __grid_constant__ NormTable tab, const __grid_constant_
 
 // T, K and the CTAs of each irrep; returns the threads of a CTA: `threads`, with
 // rows of up to that many vectors.  Plain rows may have 512 threads with up to
-// four vectors each (two of eight 16-bit channels).
+// four vectors each (two of eight 16-bit channels, 16 of one).
 template <int V>
 int shape_table(NormTable& tab, int64_t n, int threads, int& most_k, int& most_l) {
     most_l = 0;
     for (int i = 0; i < tab.n; ++i) most_l = std::max(most_l, tab.ir[i].l);
-    most_k = 1;
     const int most_t = most_l == 0 ? 512 : threads;
     if (most_l == 0) threads = 256;
+    const int least = V > 1 ? 1 : 4, most = V == 1 ? 16 : V == 8 ? 2 : 4;
+    most_k = least;
     for (int i = 0; i < tab.n; ++i) {
         NormIrrep& ir = tab.ir[i];
         const int U = ir.mul / (V == 8 && ir.l > 1 ? 4 : V);
+        ir.K = V == 1 && ir.l > 3 ? 2 : least;
         ir.T = 1;
-        ir.K = 1;
-        while (ir.T < U && ir.T < most_t) ir.T *= 2;
-        while (ir.K * ir.T < U) ir.K *= 2;
-        if (ir.K > (most_l > 0 ? 1 : V == 8 ? 2 : 4)) ir.K = 0;  // the body that reads again
-        most_k = std::max(most_k, ir.K);
+        while (ir.K * ir.T < U && ir.T < most_t) ir.T *= 2;
+        if (most_l == 0)
+            while (ir.K * ir.T < U) ir.K *= 2;
+        if (ir.K * ir.T < U || ir.K > most) ir.K = 0;  // the body that reads again
+        if (ir.l == 0) most_k = std::max(most_k, ir.K);
         threads = std::max(threads, ir.T);
     }
     tab.ctas = 0;
@@ -1041,7 +1131,9 @@ bool rows_apply(NormTable& tab, int64_t n, int& threads, int& K) {
         NormIrrep& ir = tab.ir[i];
         ir.K = K;
         ir.T = threads;
-        ir.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(ir.max_ctas, n));
+        const int most_ctas = std::min(
+            ir.max_ctas, std::max(1, ir.max_ctas * Args::kRowCtas / Args::kCtas * 256 / threads));
+        ir.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(most_ctas, n));
         ir.cta0 = tab.ctas;
         tab.ctas += ir.ctas;
     }
@@ -1058,12 +1150,13 @@ cudaError_t launch_v(NormTable tab, const Args& a, cudaStream_t s) {
                           : launch_rows<S, 4>(tab, threads, a, s);
     }
     const int threads = shape_table<V>(tab, a.n, Args::kThreads, k, l);
-    if (l > 3) return launch<S, V, 6, 1>(tab, threads, a, s);
-    if (l > 0) return launch<S, V, 3, 1>(tab, threads, a, s);
-    if (k == 1) return launch<S, V, 0, 1>(tab, threads, a, s);
+    constexpr int least = V > 1 ? 1 : 4;
+    if (l > 3) return launch<S, V, 6, least>(tab, threads, a, s);
+    if (l > 0) return launch<S, V, 3, least>(tab, threads, a, s);
+    if (k == least) return launch<S, V, 0, least>(tab, threads, a, s);
     if constexpr (V < 8)
-        if (k == 4) return launch<S, V, 0, 4>(tab, threads, a, s);
-    return launch<S, V, 0, 2>(tab, threads, a, s);
+        if (k == 4 * least) return launch<S, V, 0, 4 * least>(tab, threads, a, s);
+    return launch<S, V, 0, 2 * least>(tab, threads, a, s);
 }
 
 template <typename S, typename Args>

@@ -101,4 +101,60 @@ __device__ __forceinline__ void store_pack(S* p, const Pack<S, V>& x) {
     *reinterpret_cast<Pack<S, V>*>(p) = x;
 }
 
+// Two values that go through the arithmetic together: one packed instruction
+// for each pair of fp32 operations.
+template <typename C>
+struct Two {
+    C x, y;
+};
+__device__ __forceinline__ unsigned long long bits_of(Two<float> a) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+__device__ __forceinline__ Two<float> two_of(unsigned long long r) {
+    Two<float> a;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r));
+    return a;
+}
+__device__ __forceinline__ Two<float> fma(Two<float> a, Two<float> b, Two<float> c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(bits_of(a)), "l"(bits_of(b)), "l"(bits_of(c)));
+    return two_of(r);
+}
+__device__ __forceinline__ Two<float> operator*(Two<float> a, Two<float> b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits_of(a)), "l"(bits_of(b)));
+    return two_of(r);
+}
+__device__ __forceinline__ Two<float> operator+(Two<float> a, Two<float> b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits_of(a)), "l"(bits_of(b)));
+    return two_of(r);
+}
+__device__ __forceinline__ Two<double> fma(Two<double> a, Two<double> b, Two<double> c) {
+    return {::fma(a.x, b.x, c.x), ::fma(a.y, b.y, c.y)};
+}
+__device__ __forceinline__ Two<double> operator*(Two<double> a, Two<double> b) {
+    return {a.x * b.x, a.y * b.y};
+}
+__device__ __forceinline__ Two<double> operator+(Two<double> a, Two<double> b) {
+    return {a.x + b.x, a.y + b.y};
+}
+
+// Elements 2i and 2i + 1 of a pack.
+template <typename S, int V>
+__device__ __forceinline__ Two<typename Compute<S>::type> two_at(const Pack<S, V>& p, int i) {
+    return {p.get(2 * i), p.get(2 * i + 1)};
+}
+template <typename S, int V>
+__device__ __forceinline__ void set_twos(Pack<S, V>& p, const Two<typename Compute<S>::type> (&v)[V / 2]) {
+    typename Compute<S>::type x[V];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) x[2 * i] = v[i].x, x[2 * i + 1] = v[i].y;
+    p.set(x);
+}
+
 }  // namespace cgtp

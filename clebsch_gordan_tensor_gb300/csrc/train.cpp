@@ -74,10 +74,12 @@ static bool irrep_tables(cgtp_norm_s& h, const std::vector<Irrep>& irreps) {
         e.mul = ir.mul;
         e.off = (int)off;
         e.ch = (int)ch;
-        // a share of the CTAs by the share of the row
-        e.max_ctas = (int)std::max<int64_t>(1, kNormForwardCtas * width / h.dim);
+        // a share of the CTAs by a pair's time: its elements, and two components'
+        // worth for what a pair costs whatever its width
+        const int64_t cost = (int64_t)ir.mul * (2 * ir.l + 3), all = h.dim + 2 * h.channels;
+        e.max_ctas = (int)std::max<int64_t>(1, kNormForwardCtas * cost / all);
         h.forward.ir[i] = e;
-        e.max_ctas = (int)std::max<int64_t>(1, kNormBackwardCtas * width / h.dim);
+        e.max_ctas = (int)std::max<int64_t>(1, kNormBackwardCtas * cost / all);
         e.part0 = part;
         part += (int64_t)e.max_ctas * 2 * ir.mul;
         h.backward.ir[i] = e;
