@@ -65,6 +65,8 @@ class _Instr(ctypes.Structure):
 def lib() -> ctypes.CDLL:
     """The loaded C library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -167,7 +169,7 @@ def lib() -> ctypes.CDLL:
                                            _Rows, _Rows, _Rows, vp, vp, vp, vp, ctypes.c_size_t,
                                            vp],
                 "cgtp_adamw_layout": [i32, P(i64), P(i64), P(i64)],
-                "cgtp_adamw_step": [i32, i32, i32, i32, P(_AdamwTensor), vp, vp, vp, vp, vp, i32,
+                "cgtp_adamw_step": [i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, i32,
                                     P(_AdamwArgs), vp],
                 "cgtp_adamw_values": [i64, vp, vp, vp, vp, i32, vp, vp, vp],
             }

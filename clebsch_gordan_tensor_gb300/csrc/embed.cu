@@ -7,8 +7,9 @@
 // chunks of equal length, so that a frequent row costs no more than many rare
 // ones: a chunk adds up each run of equal keys in registers, writes the rows
 // whose run it holds whole, and leaves the first and the last run, where they
-// cross its ends, as partial rows that a second kernel joins in order.  No
-// atomics on floating-point values: the same inputs give the same bits.
+// cross its ends, as partial rows that a second kernel joins in order.  Rows
+// that no index names are zeroed beside the sums.  No atomics on floating-point
+// values: the same inputs give the same bits.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -55,9 +56,12 @@ embed_forward_kernel(int64_t n, int64_t v, int64_t d, int T, int64_t tiles,
 
 // --------------------------------------------------------------- sort --
 
-constexpr int kTile = 2048;  // positions of a CTA in a pass
+// At most one CTA an SM, each with its own range of positions, so that every
+// CTA can add up all counts before it by itself: a pass is two launches.
+constexpr int kTile = 1024;  // positions taken at a time
 constexpr int kSortThreads = 256, kSortWarps = kSortThreads / 32;
 constexpr int kPerWarp = kTile / kSortWarps;
+constexpr int kSortCtas = 152;
 
 template <typename I>
 __device__ __forceinline__ uint32_t key_of(I i, uint32_t v) {
@@ -74,113 +78,148 @@ struct Sorted {
 };
 __device__ __forceinline__ uint32_t key_of(Sorted s, uint32_t) { return s.key; }
 
+// Counts of each digit in the CTA's range, [cta][256].  The first pass also
+// clears the marks of named rows and the list of runs to join.
 template <typename I>
 __global__ void __launch_bounds__(kSortThreads)
-sort_count_kernel(uint32_t n, uint32_t v, int shift, const I* __restrict__ in,
-                  uint32_t* __restrict__ hist) {
-    __shared__ uint32_t count[256];
-    count[threadIdx.x] = 0;
+sort_count_kernel(uint32_t n, uint32_t v, uint32_t range, int shift, const I* __restrict__ in,
+                  uint32_t* __restrict__ hist, uint32_t* __restrict__ marks, uint32_t mark_words) {
+    __shared__ uint32_t count[kSortWarps][256];
+    const int warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) count[w][threadIdx.x] = 0;
+    for (uint32_t i = blockIdx.x * kSortThreads + threadIdx.x; i < mark_words;
+         i += gridDim.x * kSortThreads)
+        marks[i] = 0;
     __syncthreads();
-    const uint32_t first = blockIdx.x * kTile;
-    for (int j = threadIdx.x; j < kTile && first + j < n; j += kSortThreads)
-        atomicAdd(&count[key_of(in[first + j], v) >> shift & 255u], 1u);
+    const uint32_t first = blockIdx.x * range, last = min(first + range, n);
+    uint32_t i = first + threadIdx.x;
+    for (; i + 7 * kSortThreads < last; i += 8 * kSortThreads) {
+        I x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = in[i + j * kSortThreads];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            atomicAdd(&count[warp][key_of(x[j], v) >> shift & 255u], 1u);
+    }
+    for (; i < last; i += kSortThreads)
+        atomicAdd(&count[warp][key_of(in[i], v) >> shift & 255u], 1u);
     __syncthreads();
-    hist[threadIdx.x * gridDim.x + blockIdx.x] = count[threadIdx.x];
+    uint32_t s = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) s += count[w][threadIdx.x];
+    hist[blockIdx.x * 256 + threadIdx.x] = s;
 }
 
-// Exclusive sums of len values, one CTA.
-__global__ void __launch_bounds__(1024)
-sort_scan_kernel(uint32_t len, uint32_t* __restrict__ hist) {
-    __shared__ uint32_t warp_sum[32];
+// Stable: a warp owns consecutive positions of a tile and takes them 32 at a
+// time; a position's place is its digit's base plus the equal digits before it.
+template <typename I>
+__global__ void __launch_bounds__(kSortThreads)
+sort_scatter_kernel(uint32_t n, uint32_t v, uint32_t range, int shift, const I* __restrict__ in,
+                    const uint32_t* __restrict__ pos_in, const uint32_t* __restrict__ hist,
+                    uint32_t* __restrict__ keys, uint32_t* __restrict__ pos) {
+    __shared__ uint32_t count[kSortWarps][256];
+    __shared__ uint32_t warp_sum[kSortWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t each = (len + 1023) / 1024;
-    const uint32_t first = min(threadIdx.x * each, len), last = min(first + each, len);
-    uint32_t s = 0;
-    for (uint32_t i = first; i < last; ++i) s += hist[i];
-    uint32_t inc = s;
+    // digit threadIdx.x: its count in all CTAs and in those before this one
+    uint32_t all = 0, before = 0;
+    for (uint32_t first = 0; first < gridDim.x; first += 32) {
+        uint32_t x[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            x[j] = first + j < gridDim.x ? hist[(first + j) * 256 + threadIdx.x] : 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            all += x[j];
+            before += first + j < blockIdx.x ? x[j] : 0;
+        }
+    }
+    uint32_t inc = all;
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
         if (lane >= o) inc += x;
     }
     if (lane == 31) warp_sum[warp] = inc;
     __syncthreads();
-    if (warp == 0) {
-        uint32_t w = warp_sum[lane], x;
-        for (int o = 1; o < 32; o <<= 1) {
-            x = __shfl_up_sync(0xFFFFFFFFu, w, o);
-            if (lane >= o) w += x;
-        }
-        warp_sum[lane] = w;
-    }
-    __syncthreads();
-    uint32_t run = inc - s + (warp ? warp_sum[warp - 1] : 0);
-    for (uint32_t i = first; i < last; ++i) {
-        const uint32_t x = hist[i];
-        hist[i] = run;
-        run += x;
-    }
-}
+    uint32_t base = inc - all + before;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) base += w < warp ? warp_sum[w] : 0;
 
-// Stable: a warp owns consecutive positions and takes them 32 at a time; a
-// position's place is its digit's base plus the equal digits before it.
-template <typename I>
-__global__ void __launch_bounds__(kSortThreads)
-sort_scatter_kernel(uint32_t n, uint32_t v, int shift, const I* __restrict__ in,
-                    const uint32_t* __restrict__ pos_in, const uint32_t* __restrict__ base,
-                    uint32_t* __restrict__ keys, uint32_t* __restrict__ pos) {
-    __shared__ uint32_t count[kSortWarps][256];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int j = lane; j < 256; j += 32) count[warp][j] = 0;
-    __syncwarp();
-    const uint32_t first = blockIdx.x * kTile + warp * kPerWarp;
-    uint32_t key[kPerWarp / 32];
+    const uint32_t first = blockIdx.x * range, last = min(first + range, n);
+    for (uint32_t tile = first; tile < last; tile += kTile) {
+        __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kPerWarp / 32; ++j) {
-        const uint32_t i = first + j * 32 + lane;
-        key[j] = i < n ? key_of(in[i], v) : 0;
-        const uint32_t dig = i < n ? key[j] >> shift & 255u : 256u;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, dig);
-        if (i < n && (same & ((1u << lane) - 1)) == 0) count[warp][dig] += __popc(same);
-        __syncwarp();
-    }
-    __syncthreads();
-    {  // digit threadIdx.x: where each warp starts
-        uint32_t at = base[threadIdx.x * gridDim.x + blockIdx.x];
-        for (int w = 0; w < kSortWarps; ++w) {
-            const uint32_t c = count[w][threadIdx.x];
-            count[w][threadIdx.x] = at;
-            at += c;
-        }
-    }
-    __syncthreads();
+        for (int w = 0; w < kSortWarps; ++w) count[w][threadIdx.x] = 0;
+        __syncthreads();
+        uint32_t key[kPerWarp / 32], at[kPerWarp / 32];
+        uint32_t from[kPerWarp / 32];
 #pragma unroll
-    for (int j = 0; j < kPerWarp / 32; ++j) {
-        const uint32_t i = first + j * 32 + lane;
-        const uint32_t dig = i < n ? key[j] >> shift & 255u : 256u;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, dig);
-        const uint32_t before = same & ((1u << lane) - 1);
-        uint32_t at = 0;
-        if (i < n) {
-            at = count[warp][dig] + __popc(before);
-            keys[at] = key[j];
-            pos[at] = pos_in ? pos_in[i] : i;
+        for (int j = 0; j < kPerWarp / 32; ++j) {
+            const uint32_t i = tile + warp * kPerWarp + j * 32 + lane;
+            key[j] = i < last ? key_of(in[i], v) : 0xFFFFFFFFu;
+            from[j] = pos_in && i < last ? pos_in[i] : i;
         }
-        __syncwarp();
-        if (i < n && before == 0) count[warp][dig] += __popc(same);
-        __syncwarp();
+        // place among the warp's equal digits
+#pragma unroll
+        for (int j = 0; j < kPerWarp / 32; ++j) {
+            const bool on = key[j] != 0xFFFFFFFFu;
+            const uint32_t dig = on ? key[j] >> shift & 255u : 256u;
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, dig);
+            const uint32_t low = same & ((1u << lane) - 1);
+            at[j] = on ? count[warp][dig] + __popc(low) : 0;
+            __syncwarp();
+            if (on && low == 0) count[warp][dig] += __popc(same);
+            __syncwarp();
+        }
+        __syncthreads();
+        {
+            uint32_t x = base;
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) {
+                const uint32_t c = count[w][threadIdx.x];
+                count[w][threadIdx.x] = x;
+                x += c;
+            }
+            base = x;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kPerWarp / 32; ++j)
+            if (key[j] != 0xFFFFFFFFu) {
+                const uint32_t to = count[warp][key[j] >> shift & 255u] + at[j];
+                keys[to] = key[j];
+                pos[to] = from[j];
+            }
     }
 }
 
 // --------------------------------------------------------------- sums --
 
-// One group of T lanes: the runs of chunk c in the columns of one tile.
+template <typename C, int V>
+__device__ __forceinline__ void store_sums(C* p, const C (&x)[V]) {
+    constexpr int W = V * sizeof(C) >= 16 ? 16 / sizeof(C) : V;
+#pragma unroll
+    for (int k = 0; k < V; k += W) {
+        Pack<C, W> o;
+#pragma unroll
+        for (int i = 0; i < W; ++i) o.v[i] = x[k + i];
+        store_pack(p + k, o);
+    }
+}
+
+constexpr int kSumCtas = 3;  // resident on an SM
+
+// One group of T lanes: the runs of chunk c in the columns of one tile.  Marks
+// the rows that it meets.
 template <typename S, int V>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, kSumCtas)
 embed_sum_kernel(uint32_t n, uint32_t v, int64_t d, int T, uint32_t tiles, uint32_t chunk,
                  uint32_t chunks, const uint32_t* __restrict__ keys,
-                 const uint32_t* __restrict__ pos, const S* __restrict__ g, int64_t stride,
-                 typename Compute<S>::type scale, S* __restrict__ table,
-                 typename Compute<S>::type* __restrict__ partial) {
+                 const uint32_t* __restrict__ pos, uint8_t* __restrict__ marks,
+                 const S* __restrict__ g, int64_t stride, typename Compute<S>::type scale,
+                 S* __restrict__ table, typename Compute<S>::type* __restrict__ partial,
+                 uint32_t* __restrict__ list) {
     using C = typename Compute<S>::type;
     const int64_t w = (int64_t)blockIdx.x * (256 / T) + threadIdx.x / T;
     const uint32_t c = (uint32_t)(w / tiles);
@@ -192,10 +231,12 @@ embed_sum_kernel(uint32_t n, uint32_t v, int64_t d, int T, uint32_t tiles, uint3
     bool head = first > 0 && keys[first - 1] == cur;
     C acc[V] = {};
     auto finish = [&](bool tail) {
+        if (col == 0) {
+            marks[cur] = 1;
+            if (tail && !head) list[1 + atomicAdd(list, 1u)] = c;  // joined in any order
+        }
         if (head || tail) {
-            C* p = partial + ((int64_t)c * 2 + (head ? 0 : 1)) * d + col;
-#pragma unroll
-            for (int k = 0; k < V; ++k) p[k] = acc[k];
+            store_sums(partial + ((int64_t)c * 2 + (head ? 0 : 1)) * d + col, acc);
         } else {
             Pack<S, V> o;
 #pragma unroll
@@ -204,15 +245,26 @@ embed_sum_kernel(uint32_t n, uint32_t v, int64_t d, int T, uint32_t tiles, uint3
             store_pack(table + (int64_t)cur * d + col, o);
         }
     };
-    constexpr int U = 4;  // rows in flight
+    // Eight rows in flight, and the positions of the next eight.  A row's address
+    // needs no key: padding sorts last, and its rows exist.
+    constexpr int U = 8;  // chunks are multiples of it
+    uint4 pq[2];
+    auto positions = [&](uint32_t j) {
+        pq[0] = *reinterpret_cast<const uint4*>(pos + j);
+        pq[1] = *reinterpret_cast<const uint4*>(pos + j + 4);
+    };
+    positions(first);
     for (uint32_t j = first; j < last; j += U) {
-        uint32_t key[U];
+        const uint32_t from[U] = {pq[0].x, pq[0].y, pq[0].z, pq[0].w,
+                                  pq[1].x, pq[1].y, pq[1].z, pq[1].w};
         Pack<S, V> row[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            key[u] = j + u < last ? keys[j + u] : v;
-            if (key[u] < v) row[u] = load_pack<S, V>(g + (int64_t)pos[j + u] * stride + col);
-        }
+        for (int u = 0; u < U; ++u)
+            if (j + u < last) row[u] = load_pack<S, V>(g + (int64_t)from[u] * stride + col);
+        const uint4 k0 = *reinterpret_cast<const uint4*>(keys + j);
+        const uint4 k1 = *reinterpret_cast<const uint4*>(keys + j + 4);
+        if (j + U < last) positions(j + U);
+        const uint32_t key[U] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (j + u >= last) break;
@@ -231,39 +283,139 @@ embed_sum_kernel(uint32_t n, uint32_t v, int64_t d, int T, uint32_t tiles, uint3
     finish(last < n && keys[last] == cur);
 }
 
-// The runs that start in chunk c and go on past its end.
+// The sums of the partial rows [from, to) of the run that starts in chunk c:
+// the second row of that chunk, then the first rows of the next ones.
+template <typename C, int V>
+__device__ __forceinline__ void add_run(C (&acc)[V], const C* partial, int64_t d, int64_t col,
+                                        uint32_t c, uint32_t from, uint32_t to) {
+    for (uint32_t first = from; first < to; first += 8) {
+        Pack<C, V> x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t i = first + j;
+            x[j].fill(0);
+            if (i < to)
+                x[j] = load_pack<C, V>(partial + ((int64_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * d + col);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int k = 0; k < V; ++k) acc[k] += x[j].v[k];
+    }
+}
+
+// The runs that cross chunks, from the list, each in tiles of T * V columns.  A
+// warp takes a run and tile; one of many chunks is left to its whole CTA.  Lanes
+// (warps) of one column add consecutive shares of the run's rows, whose sums are
+// then added in order.  CTAs past join_ctas zero the rows without a mark.
 template <typename S, int V>
 __global__ void __launch_bounds__(256)
-embed_join_kernel(uint32_t n, uint32_t v, int64_t d, int T, uint32_t tiles, uint32_t chunk,
-                  uint32_t chunks, const uint32_t* __restrict__ keys,
-                  typename Compute<S>::type scale, S* __restrict__ table,
-                  const typename Compute<S>::type* __restrict__ partial) {
+embed_join_kernel(uint32_t v, int64_t d, int T, uint32_t tiles, uint32_t chunk, uint32_t chunks,
+                  uint32_t join_ctas, const uint32_t* __restrict__ keys,
+                  const uint8_t* __restrict__ marks, typename Compute<S>::type scale,
+                  S* __restrict__ table, const typename Compute<S>::type* __restrict__ partial,
+                  const uint32_t* __restrict__ list) {
     using C = typename Compute<S>::type;
-    const int64_t w = (int64_t)blockIdx.x * (256 / T) + threadIdx.x / T;
-    uint32_t c = (uint32_t)(w / tiles);
-    const int64_t col = (w % tiles * T + threadIdx.x % T) * V;
-    if (c >= chunks || col >= d) return;
-    const uint32_t first = c * chunk, last = min(first + chunk, n);
-    if (last >= n) return;
-    const uint32_t cur = keys[last];
-    if (cur >= v || keys[last - 1] != cur) return;
-    if (keys[first] == cur && first > 0 && keys[first - 1] == cur) return;  // it starts earlier
-    C acc[V];
-    const C* p = partial + ((int64_t)c * 2 + 1) * d + col;
-#pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = p[k];
-    for (++c;; ++c) {
-        p = partial + (int64_t)c * 2 * d + col;
-#pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] += p[k];
-        const int64_t end = (int64_t)(c + 1) * chunk;
-        if (end >= n || keys[end] != cur) break;
+    constexpr uint32_t kLong = 32;  // chunks: above it, eight warps
+    __shared__ C part[8][32 * V];
+    __shared__ uint32_t run_c[8], run_rows[8], run_key[8], run_tile[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (blockIdx.x >= join_ctas) {
+        const uint32_t warps = (gridDim.x - join_ctas) * 8;
+        Pack<S, V> zero;
+        zero.fill((C)0);
+        for (uint32_t r = (blockIdx.x - join_ctas) * 8 + warp; r < v; r += warps)
+            if (!marks[r])
+                for (int64_t c = lane * V; c < d; c += 32 * V)
+                    store_pack(table + (int64_t)r * d + c, zero);
+        return;
     }
-    Pack<S, V> o;
+    const uint64_t items = (uint64_t)list[0] * tiles;
+    const int t = lane % T, shares = 32 / T;
+    auto write = [&](C (&acc)[V], uint32_t cur, int64_t col) {
+        Pack<S, V> o;
 #pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] *= scale;
-    o.set(acc);
-    store_pack(table + (int64_t)cur * d + col, o);
+        for (int k = 0; k < V; ++k) acc[k] *= scale;
+        o.set(acc);
+        store_pack(table + (int64_t)cur * d + col, o);
+    };
+    // a share of a warp's lanes each, added in order; the result in share 0
+    auto add_shares = [&](C (&acc)[V]) {
+        for (int q = 1; q < shares; ++q)
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const C x = __shfl_sync(0xFFFFFFFFu, acc[k], q * T + t);
+                if (lane < T) acc[k] += x;
+            }
+    };
+    // consecutive items go to different CTAs: long runs come one after another
+    for (uint64_t base = blockIdx.x; base < items; base += (uint64_t)join_ctas * 8) {
+        const uint64_t item = base + (uint64_t)warp * join_ctas;
+        uint32_t rows = 0;
+        if (item < items) {
+            const uint32_t c = list[1 + item / tiles];
+            const uint32_t cur = keys[(int64_t)(c + 1) * chunk];  // the run goes on there
+            // the first chunk not to start with it, among the next 32, then by
+            // 32 probes at a time in what is left
+            uint32_t lo = c + 2, hi = min(lo + 32, chunks);
+            for (bool near = true;; near = false) {
+                const uint32_t step = (hi - lo + 31) / 32, at = lo + lane * step;
+                const bool go = at < hi && keys[(int64_t)at * chunk] == cur;
+                const uint32_t miss = ~__ballot_sync(0xFFFFFFFFu, go);
+                const uint32_t on = miss ? __ffs(miss) - 1 : 32;  // probes that go on
+                if (near && on == 32 && hi < chunks) {
+                    lo = hi, hi = chunks;
+                    continue;
+                }
+                if (step <= 1) {
+                    lo = min(lo + on, hi);
+                    break;
+                }
+                hi = min(lo + on * step, hi);  // misses here, or the end
+                lo = on ? lo + (on - 1) * step + 1 : lo;
+                if (on == 0) break;
+            }
+            rows = lo - c;
+            if (rows <= kLong) {
+                const uint32_t share = (rows + shares - 1) / shares;
+                const uint32_t from = min(lane / T * share, rows), to = min(from + share, rows);
+                const int64_t col = ((int64_t)(item % tiles) * T + t) * V;
+                C acc[V] = {};
+                if (col < d) add_run(acc, partial, d, col, c, from, to);
+                add_shares(acc);
+                if (lane < T && col < d) write(acc, cur, col);
+            }
+            if (lane == 0) {
+                run_c[warp] = c;
+                run_key[warp] = cur;
+                run_tile[warp] = (uint32_t)(item % tiles);
+            }
+        }
+        if (lane == 0) run_rows[warp] = rows;
+        __syncthreads();
+        for (int r = 0; r < 8; ++r) {
+            const uint32_t all = run_rows[r];
+            if (all <= kLong) continue;
+            const uint32_t share = (all + 8 * shares - 1) / (8 * shares);
+            const uint32_t from = min((warp * shares + lane / T) * share, all);
+            const int64_t col = ((int64_t)run_tile[r] * T + t) * V;
+            C acc[V] = {};
+            if (col < d)
+                add_run(acc, partial, d, col, run_c[r], from, min(from + share, all));
+            add_shares(acc);
+#pragma unroll
+            for (int k = 0; k < V; ++k) part[warp][lane * V + k] = acc[k];
+            __syncthreads();
+            if (warp == 0 && lane < T && col < d) {
+                for (int w = 1; w < 8; ++w)
+#pragma unroll
+                    for (int k = 0; k < V; ++k) acc[k] += part[w][lane * V + k];
+                write(acc, run_key[r], col);
+            }
+            __syncthreads();
+        }
+        __syncthreads();
+    }
 }
 
 __global__ void __launch_bounds__(256) embed_zero_kernel(uint8_t* __restrict__ p, int64_t bytes) {
@@ -290,31 +442,36 @@ uint32_t blocks_for(int64_t groups, int T) {
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
-// Positions of a chunk: enough chunks to fill the GPU, few enough that their
-// partial rows stay small beside the gradient rows.
-uint32_t chunk_of(int64_t n, int64_t d) {
-    const int64_t tiles = (d + 127) / 128, want = 152 * 32;
-    int64_t c = n * tiles / want;
-    c = std::max<int64_t>(16, std::min<int64_t>(c, 256));
-    return (uint32_t)c;
+// Positions of a chunk: all warps resident at once, and not so few positions
+// that partial rows add up.
+uint32_t chunk_of(int64_t n, int64_t vecs) {
+    const int64_t T = lanes_for(vecs), tiles = (vecs + T - 1) / T;
+    const int64_t warps = 152 * kSumCtas * 8, c = (n * tiles * T + 32 * warps - 1) / (32 * warps);
+    return (uint32_t)std::max<int64_t>(16, std::min<int64_t>((c + 7) / 8 * 8, 256));
 }
 
 struct Layout {
-    uint32_t chunk, chunks, sort_ctas;
-    size_t keys[2], pos[2], hist, partial, total;
+    uint32_t chunk, chunks, sort_ctas, range;
+    size_t keys[2], pos[2], hist, list, marks, partial, total;
 };
 
-Layout layout_of(cgtp_dtype type, int64_t n, int64_t d) {
+Layout layout_of(cgtp_dtype type, int64_t n, int64_t v, int64_t d) {
     Layout L;
-    L.chunk = chunk_of(n, d);
+    const int64_t each = type == CGTP_F64 ? 2 : type == CGTP_F32 ? 4 : 8;
+    L.chunk = chunk_of(n, (d + each - 1) / each);
     L.chunks = (uint32_t)((n + L.chunk - 1) / L.chunk);
-    L.sort_ctas = (uint32_t)((n + kTile - 1) / kTile);
+    L.sort_ctas = (uint32_t)std::min<int64_t>(kSortCtas, (n + kTile - 1) / kTile);
+    // whole tiles, but for the last
+    L.range = (uint32_t)(((n + L.sort_ctas - 1) / L.sort_ctas + kTile - 1) / kTile * kTile);
     size_t at = 0;
-    for (int k = 0; k < 2; ++k) {
-        L.keys[k] = at, at += up256((size_t)n * 4);
-        L.pos[k] = at, at += up256((size_t)n * 4);
+    for (int k = 0; k < 2; ++k) {  // read eight at a time
+        L.keys[k] = at, at += up256((size_t)n * 4 + 64);
+        L.pos[k] = at, at += up256((size_t)n * 4 + 64);
     }
     L.hist = at, at += up256((size_t)L.sort_ctas * 256 * 4);
+    // cleared together: the marks, then the list's length
+    L.marks = at, at += ((size_t)v + 3) / 4 * 4;
+    L.list = at, at = up256(at + ((size_t)L.chunks + 1) * 4);
     L.partial = at;
     at += up256((size_t)L.chunks * 2 * (size_t)d * (type == CGTP_F64 ? 8 : 4));
     L.total = at;
@@ -327,31 +484,42 @@ cudaError_t sort_pass(const EmbedCall& c, const Layout& L, int shift, const I* i
     uint8_t* ws = (uint8_t*)c.ws;
     uint32_t* hist = (uint32_t*)(ws + L.hist);
     const uint32_t n = (uint32_t)c.n, v = (uint32_t)c.v;
-    sort_count_kernel<I><<<L.sort_ctas, kSortThreads, 0, s>>>(n, v, shift, in, hist);
-    sort_scan_kernel<<<1, 1024, 0, s>>>(L.sort_ctas * 256, hist);
+    const bool first = pos_in == nullptr;
+    const uint32_t words = first ? (uint32_t)((L.list - L.marks) / 4 + 1) : 0;
+    sort_count_kernel<I><<<L.sort_ctas, kSortThreads, 0, s>>>(
+        n, v, L.range, shift, in, hist, (uint32_t*)(ws + L.marks), words);
     sort_scatter_kernel<I><<<L.sort_ctas, kSortThreads, 0, s>>>(
-        n, v, shift, in, pos_in, hist, (uint32_t*)(ws + L.keys[to]), (uint32_t*)(ws + L.pos[to]));
-    for (int k = 0; k < 3; ++k) count_launch();
+        n, v, L.range, shift, in, pos_in, hist, (uint32_t*)(ws + L.keys[to]),
+        (uint32_t*)(ws + L.pos[to]));
+    count_launch();
+    count_launch();
     return cudaGetLastError();
 }
 
-template <typename S, int V>
+// V: elements of an access; J: sums of one in the join.
+template <typename S, int V, int J>
 cudaError_t backward_v(const EmbedCall& c, const Layout& L, int sorted, cudaStream_t s) {
     using C = typename Compute<S>::type;
     uint8_t* ws = (uint8_t*)c.ws;
     const uint32_t* keys = (const uint32_t*)(ws + L.keys[sorted]);
     const uint32_t* pos = (const uint32_t*)(ws + L.pos[sorted]);
+    uint32_t* list = (uint32_t*)(ws + L.list);
     const int T = lanes_for((c.d + V - 1) / V);
     const uint32_t tiles = (uint32_t)((c.d + (int64_t)T * V - 1) / ((int64_t)T * V));
-    const uint32_t grid = blocks_for((int64_t)L.chunks * tiles, T);
-    embed_sum_kernel<S, V><<<grid, 256, 0, s>>>((uint32_t)c.n, (uint32_t)c.v, c.d, T, tiles,
-                                                L.chunk, L.chunks, keys, pos, (const S*)c.in,
-                                                c.in_stride, (C)c.scale, (S*)c.out,
-                                                (C*)(ws + L.partial));
-    embed_join_kernel<S, V><<<grid, 256, 0, s>>>((uint32_t)c.n, (uint32_t)c.v, c.d, T, tiles,
-                                                 L.chunk, L.chunks, keys, (C)c.scale, (S*)c.out,
-                                                 (const C*)(ws + L.partial));
+    embed_sum_kernel<S, V><<<blocks_for((int64_t)L.chunks * tiles, T), 256, 0, s>>>(
+        (uint32_t)c.n, (uint32_t)c.v, c.d, T, tiles, L.chunk, L.chunks, keys, pos, ws + L.marks,
+        (const S*)c.in, c.in_stride, (C)c.scale, (S*)c.out, (C*)(ws + L.partial), list);
     count_launch();
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int TJ = lanes_for((c.d + J - 1) / J);
+    const uint32_t join_tiles = (uint32_t)((c.d + (int64_t)TJ * J - 1) / ((int64_t)TJ * J));
+    const uint32_t joins =
+        (uint32_t)std::min<int64_t>(((int64_t)L.chunks * join_tiles + 7) / 8, 152 * 6);
+    const uint32_t zeros = (uint32_t)std::min<int64_t>((c.v + 7) / 8, 152 * 2);
+    embed_join_kernel<S, J><<<joins + zeros, 256, 0, s>>>(
+        (uint32_t)c.v, c.d, TJ, join_tiles, L.chunk, L.chunks, joins, keys, ws + L.marks,
+        (C)c.scale, (S*)c.out, (const C*)(ws + L.partial), list);
     count_launch();
     return cudaGetLastError();
 }
@@ -366,13 +534,15 @@ bool wide(const EmbedCall& c) {
 
 template <typename S>
 cudaError_t backward(const EmbedCall& c, cudaStream_t s) {
-    const int64_t bytes = c.v * c.d * (int64_t)sizeof(S);
-    embed_zero_kernel<<<(unsigned)std::min<int64_t>((bytes / 16 + 255) / 256 + 1, 152 * 16), 256, 0,
-                        s>>>((uint8_t*)c.out, bytes);
-    count_launch();
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || c.n == 0) return e;
-    const Layout L = layout_of(c.type, c.n, c.d);
+    cudaError_t e;
+    if (c.n == 0) {
+        const int64_t bytes = c.v * c.d * (int64_t)sizeof(S);
+        const unsigned grid = (unsigned)std::min<int64_t>(bytes / 4096 + 1, 152 * 16);
+        embed_zero_kernel<<<grid, 256, 0, s>>>((uint8_t*)c.out, bytes);
+        count_launch();
+        return cudaGetLastError();
+    }
+    const Layout L = layout_of(c.type, c.n, c.v, c.d);
     uint8_t* ws = (uint8_t*)c.ws;
     int bits = 1;
     while (((int64_t)1 << bits) <= c.v) ++bits;  // keys 0..V
@@ -387,8 +557,9 @@ cudaError_t backward(const EmbedCall& c, cudaStream_t s) {
                           (const uint32_t*)(ws + L.pos[to ^ 1]), to, s);
         if (e != cudaSuccess) return e;
     }
-    return wide<S>(c) ? backward_v<S, 16 / sizeof(S)>(c, L, to ^ 1, s)
-                      : backward_v<S, 1>(c, L, to ^ 1, s);
+    constexpr int V = 16 / sizeof(S), J = sizeof(S) == 8 ? 2 : 4;
+    return wide<S>(c) ? backward_v<S, V, J>(c, L, to ^ 1, s)
+                      : backward_v<S, 1, 1>(c, L, to ^ 1, s);
 }
 
 template <typename S, typename I, int V>
@@ -425,8 +596,7 @@ cudaError_t launch_embed_forward(const EmbedCall& c, cudaStream_t s) {
 }
 
 size_t embed_backward_workspace_bytes(cgtp_dtype type, int64_t n, int64_t v, int64_t d) {
-    (void)v;
-    return n == 0 ? 0 : layout_of(type, n, d).total;
+    return n == 0 ? 0 : layout_of(type, n, v, d).total;
 }
 
 cudaError_t launch_embed_backward(const EmbedCall& c, cudaStream_t s) {

@@ -27,6 +27,8 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "internal.hpp"
 #include "storage.cuh"
@@ -104,6 +106,23 @@ __device__ __forceinline__ void load_param(C (&out)[V], const C* p, int at, C mi
 template <typename S>
 __device__ __forceinline__ S* row_of(const cgtp_rows& q, int64_t row, int at) {
     return q.data ? (S*)q.data + row * q.stride + at : nullptr;
+}
+
+// Asynchronous copies to shared memory of 4, 8 or 16 bytes.
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N)
+                     : "memory");
+}
+__device__ __forceinline__ void copies_end_group() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // ------------------------------------------------------------- forward --
@@ -388,10 +407,89 @@ __device__ __forceinline__ void load_backward(BackwardRegs<S, V, L, K>& q, const
         }
 }
 
+// The next row of a thread's vectors, on its way through shared memory while
+// the current one is worked on: with five components or more in registers there
+// is no room for a second row there.  A thread reads what it copied itself, so
+// no barrier is needed.  Slots of absent tensors and of threads past the last
+// channel keep the values they are filled with.
+template <typename S, int V, int L, int K>
+struct BackwardRing {
+    static constexpr int M = 2 * L + 1, N = V * sizeof(S);
+    unsigned char* mine;
+    __device__ __forceinline__ Pack<S, V>* slot(int tensor, int k, int m) const {
+        return reinterpret_cast<Pack<S, V>*>(
+            mine + (size_t)((tensor * M + m) * K + k) * blockDim.x * N);
+    }
+    __device__ __forceinline__ BackwardRing(unsigned char* all) : mine(all + threadIdx.x * N) {
+        const BackwardRegs<S, V, L, K> q;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                *slot(0, k, m) = q.b[k][m];
+                *slot(1, k, m) = q.h[k][m];
+                *slot(2, k, m) = q.gh[k][m];
+                *slot(3, k, m) = q.gy[k][m];
+            }
+            *slot(4, k, 0) = q.z[k];
+        }
+    }
+    __device__ __forceinline__ void fetch(const NormIrrep& ir, const NormBackward& a, int64_t row,
+                                          int t) {
+        if (row < a.n) {
+            const S *b = row_of<const S>(a.b, row, ir.off), *h = row_of<const S>(a.h, row, ir.off);
+            const S *gh = row_of<const S>(a.grad_h, row, ir.off);
+            const S *gy = row_of<const S>(a.grad_y, row, ir.off);
+            const S* z = row_of<const S>(a.gate, row, ir.ch);
+            auto get = [&](int tensor, int k, int m, const S* p) {
+                copy_async<N>((uint32_t)__cvta_generic_to_shared(slot(tensor, k, m)), p);
+            };
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (t + k * ir.T < ir.mul / V) {
+                    const int u = (t + k * ir.T) * V;
+#pragma unroll
+                    for (int m = 0; m < M; ++m) {
+                        get(0, k, m, b + m * ir.mul + u);
+                        if (gy) get(1, k, m, h + m * ir.mul + u);
+                        if (gh) get(2, k, m, gh + m * ir.mul + u);
+                        if (gy) get(3, k, m, gy + m * ir.mul + u);
+                    }
+                    if (z) get(4, k, 0, z + u);
+                }
+        }
+        copies_end_group();
+    }
+    __device__ __forceinline__ void read(BackwardRegs<S, V, L, K>& q, bool in) const {
+        copies_wait<0>();
+        if (!in) {  // adds nothing to the channel sums
+            q = BackwardRegs<S, V, L, K>();
+            return;
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                q.b[k][m] = *slot(0, k, m);
+                q.h[k][m] = *slot(1, k, m);
+                q.gh[k][m] = *slot(2, k, m);
+                q.gy[k][m] = *slot(3, k, m);
+            }
+            q.z[k] = *slot(4, k, 0);
+        }
+    }
+};
+// Bytes a thread needs there.
+template <typename S, int V, int L>
+constexpr int kRingBytes =
+    L == 0 || kWidth<V, L> * sizeof(S) < 4
+        ? 0
+        : (4 * (2 * L + 1) + 1) * kEach<V, L> * kWidth<V, L> * (int)sizeof(S);
+
 template <typename S, int V, int L, int K>
 __device__ __forceinline__ void backward_body(const NormIrrep& ir, int cta, const NormBackward& a,
                                               typename Compute<S>::type (*sums)[kMaxWarps],
-                                              typename Compute<S>::type* rows) {
+                                              unsigned char* dynamic) {
     using C = typename Compute<S>::type;
     constexpr int M = 2 * L + 1;
     const int T = ir.T, t = threadIdx.x % T, G = blockDim.x / T;
@@ -416,11 +514,24 @@ __device__ __forceinline__ void backward_body(const NormIrrep& ir, int cta, cons
     const int64_t step = (int64_t)ir.ctas * G;
     int64_t row = (int64_t)cta * G + threadIdx.x / T;
     constexpr bool kAhead = L == 0 && K * V * sizeof(S) <= 16;
+    constexpr bool kRing = L > 0 && V * sizeof(S) >= 4;
     BackwardRegs<S, V, L, K> q, ahead;
-    load_backward(q, ir, a, row, t);
+    struct None {
+        __device__ None(unsigned char*) {}
+    };
+    using Ring = std::conditional_t<kRing, BackwardRing<S, V, L, K>, None>;
+    Ring ring(dynamic);
+    if constexpr (kRing)
+        ring.fetch(ir, a, row, t);
+    else
+        load_backward(q, ir, a, row, t);
     for (int64_t base = (int64_t)cta * G; base < a.n; base += step, row += step) {
         if constexpr (kAhead) load_backward(ahead, ir, a, row + step, t);
         const bool in = row < a.n;
+        if constexpr (kRing) {
+            ring.read(q, in);
+            ring.fetch(ir, a, row + step, t);
+        }
         C s[3] = {0, 0, 0};  // b^2, h^2, next_weight gy h
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -500,11 +611,13 @@ __device__ __forceinline__ void backward_body(const NormIrrep& ir, int cta, cons
             }
         if constexpr (kAhead)
             q = ahead;
-        else
+        else if constexpr (!kRing)
             load_backward(q, ir, a, row + step, t);
     }
+    if constexpr (kRing) copies_wait<0>();
     if (!a.partial) return;
     // The groups' sums, added in group order through shared memory.
+    C* rows = reinterpret_cast<C*>(dynamic);
     C* out = partial_row<C>(ir, cta, a);
     auto flush = [&](C (&acc)[K][V], int which) {
         __syncthreads();
@@ -643,12 +756,11 @@ norm_backward_kernel(const __grid_constant__ NormTable tab,
     using C = typename Compute<S>::type;
     __shared__ C sums[6][kMaxWarps];
     extern __shared__ __align__(16) unsigned char dynamic[];
-    C* rows = reinterpret_cast<C*>(dynamic);
     int i = 0;
     while (i + 1 < tab.n && (int)blockIdx.x >= tab.ir[i + 1].cta0) ++i;
     const NormIrrep& ir = tab.ir[i];
     const int cta = blockIdx.x - ir.cta0;
-#define CALL(L, K) backward_body<S, kWidth<V, L>, L, K>(ir, cta, a, sums, rows)
+#define CALL(L, K) backward_body<S, kWidth<V, L>, L, K>(ir, cta, a, sums, dynamic)
     CGTP_NORM_BODIES(LC, V, K, CALL, (backward_wide<S, V>(ir, cta, a, sums)))
 #undef CALL
 }
@@ -664,17 +776,6 @@ norm_backward_kernel(const __grid_constant__ NormTable tab,
 // thread copying the vectors that it reads itself: no registers for rows in
 // flight and no barrier or wait on another thread.
 constexpr int kStages = 2;
-
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copies_end_group() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 // A thread's vectors of N tensors in kStages stages; tensor j's vector k of
 // stage s at ((s N + j) K + k) threads + thread, 16 bytes each.
@@ -702,7 +803,7 @@ struct RowRing {
         for (int k = 0; k < K; ++k) {
             const int u = threadIdx.x + k * blockDim.x;
             if (u < U)
-                copy_async((uint32_t)__cvta_generic_to_shared(slot(s, j, k)), p + u * V);
+                copy_async<16>((uint32_t)__cvta_generic_to_shared(slot(s, j, k)), p + u * V);
         }
     }
     __device__ __forceinline__ Pack<S, V> get(int s, int j, int k) const {
@@ -1056,6 +1157,18 @@ int shape_table(NormTable& tab, int64_t n, int threads, int& most_k, int& most_l
     return threads;
 }
 
+// Lets a kernel take up to 224 KB of dynamic shared memory, once a device.
+inline cudaError_t allow_smem(const void* f, std::atomic<uint32_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint32_t bit = 1u << (dev & 31);
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 << 10);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 template <typename C>
 cudaError_t finish(const NormTable&, const NormForward&, cudaStream_t) {
     return cudaSuccess;
@@ -1078,11 +1191,22 @@ cudaError_t launch(const NormTable& tab, int threads, const NormForward& a, cuda
 template <typename S, int V, int LC, int K>
 cudaError_t launch(const NormTable& tab, int threads, const NormBackward& a, cudaStream_t s) {
     using C = typename Compute<S>::type;
-    // one set of channel sums of every thread
-    const int smem = a.partial ? threads * K * V * (int)sizeof(C) : 0;
+    // one set of channel sums of every thread, and before that the rows ahead
+    int each = a.partial ? std::max(K * V, 4) * (int)sizeof(C) : 0;
+    for (int i = 0; i < tab.n; ++i) {
+        constexpr int ring[] = {0,
+                                kRingBytes<S, V, 1>,
+                                kRingBytes<S, V, 2>,
+                                kRingBytes<S, V, 3>,
+                                kRingBytes<S, V, 4>,
+                                kRingBytes<S, V, 5>,
+                                kRingBytes<S, V, 6>};
+        if (tab.ir[i].K) each = std::max(each, ring[tab.ir[i].l]);
+    }
+    const int smem = threads * each;
     if (smem > 48 << 10) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            norm_backward_kernel<S, V, LC, K>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        static std::atomic<uint32_t> done{0};
+        const cudaError_t e = allow_smem((const void*)norm_backward_kernel<S, V, LC, K>, done);
         if (e != cudaSuccess) return e;
     }
     norm_backward_kernel<S, V, LC, K><<<tab.ctas, threads, smem, s>>>(tab, a);
@@ -1103,8 +1227,8 @@ template <typename S, int K, typename Args>
 cudaError_t launch_rows(const NormTable& tab, int threads, const Args& a, cudaStream_t s) {
     const void* f = row_kernel<S, K>(a);
     const size_t smem = (size_t)kStages * Args::kInputs * K * threads * 16;
-    cudaError_t e =
-        cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint32_t> done{0};
+    cudaError_t e = allow_smem(f, done);
     if (e != cudaSuccess) return e;
     void* args[] = {const_cast<NormTable*>(&tab), const_cast<Args*>(&a)};
     e = cudaLaunchKernel(f, dim3(tab.ctas), dim3(threads), args, smem, s);
@@ -1161,11 +1285,13 @@ cudaError_t launch_v(NormTable tab, const Args& a, cudaStream_t s) {
 
 template <typename S, typename Args>
 cudaError_t launch_norm(const NormTable& tab, const Args& a, int vector, cudaStream_t s) {
-    if constexpr (sizeof(S) == 8)
+    if constexpr (sizeof(S) == 8) {
         return vector >= 2 ? launch_v<S, 2>(tab, a, s) : launch_v<S, 1>(tab, a, s);
-    if constexpr (sizeof(S) == 2)
-        if (vector == 8) return launch_v<S, 8>(tab, a, s);
-    return vector >= 4 ? launch_v<S, 4>(tab, a, s) : launch_v<S, 1>(tab, a, s);
+    } else {
+        if constexpr (sizeof(S) == 2)
+            if (vector == 8) return launch_v<S, 8>(tab, a, s);
+        return vector >= 4 ? launch_v<S, 4>(tab, a, s) : launch_v<S, 1>(tab, a, s);
+    }
 }
 
 }  // namespace

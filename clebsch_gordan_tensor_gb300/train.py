@@ -9,12 +9,26 @@ from __future__ import annotations
 
 import ctypes
 
+import numpy as np
 import torch
 
-from . import (BF16, F16, F32, F64, CgtpError, _AdamwArgs, _AdamwTensor, _check, _need, _ptr,
-               _Rows, _stream, lib)
+from . import BF16, F16, F32, F64, CgtpError, _AdamwArgs, _check, _need, _Rows, _stream, lib
 
 _TYPES = {torch.float32: F32, torch.float64: F64, torch.bfloat16: BF16, torch.float16: F16}
+_NONE = _Rows(None, 0)
+
+# The small calls here are as long as their Python: the raw stream spares a
+# Stream object a call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on():
+    """The current stream's handle."""
+    return _stream() if _raw_stream is None else _raw_stream(torch.cuda.current_device())
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _type(dtype) -> int:
@@ -23,19 +37,20 @@ def _type(dtype) -> int:
     return _TYPES[dtype]
 
 
-def _rows(t, name, dtype, shape):
+def _rows(t, name, dtype, n, width):
     """Rows of a tensor, which may lie further apart than they are wide."""
     if t is None:
-        return _Rows(None, 0)
+        return _NONE
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise CgtpError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise CgtpError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise CgtpError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.stride(1) != 1 and shape[1] != 1:
+    if t.shape != (n, width):
+        raise CgtpError(f"{name} has shape {tuple(t.shape)}, expected {(n, width)}")
+    step, inner = t.stride()
+    if inner != 1 and width != 1:
         raise CgtpError(f"{name} must have contiguous rows")
-    return _Rows(t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1])
+    return _Rows(t.data_ptr(), step if n > 1 else width)
 
 
 def _scratch(nbytes, device):
@@ -67,9 +82,12 @@ def embed_forward(index, table, scale: float = 1.0, out=None):
     n, (v, d) = index.shape[0], table.shape
     if out is None:
         out = torch.empty(n, d, dtype=table.dtype, device=table.device)
-    o = _rows(out, "out", table.dtype, (n, d))
-    _check(lib().cgtp_embed_forward(_type(table.dtype), bits, n, v, d, _ptr(index), _ptr(table),
-                                    float(scale), o.data, o.stride, _stream()))
+        o, step = out.data_ptr(), d
+    else:
+        o = _rows(out, "out", table.dtype, n, d)
+        o, step = o.data, o.stride
+    _check(lib().cgtp_embed_forward(_type(table.dtype), bits, n, v, d, index.data_ptr(),
+                                    table.data_ptr(), float(scale), o, step, _on()))
     return out
 
 
@@ -82,18 +100,19 @@ def embed_backward(index, grad_out, n_rows: int, scale: float = 1.0, out=None, w
     if not isinstance(grad_out, torch.Tensor) or grad_out.dim() != 2:
         raise CgtpError("grad_out must be a tensor of rows")
     d = grad_out.shape[1]
-    g = _rows(grad_out, "grad_out", grad_out.dtype, (n, d))
+    g = _rows(grad_out, "grad_out", grad_out.dtype, n, d)
     if out is None:
         out = torch.empty(n_rows, d, dtype=grad_out.dtype, device=grad_out.device)
-    _need(out, "out", grad_out.dtype, (n_rows, d))
+    else:
+        _need(out, "out", grad_out.dtype, (n_rows, d))
     ty = _type(grad_out.dtype)
     if workspace is None:
         nb = ctypes.c_size_t()
         _check(lib().cgtp_embed_backward_workspace(ty, n, n_rows, d, ctypes.byref(nb)))
         workspace = _scratch(nb.value, grad_out.device)
-    _check(lib().cgtp_embed_backward(ty, bits, n, n_rows, d, _ptr(index), g.data, g.stride,
-                                     float(scale), _ptr(out), _ptr(workspace),
-                                     workspace.numel() * workspace.element_size(), _stream()))
+    _check(lib().cgtp_embed_backward(ty, bits, n, n_rows, d, index.data_ptr(), g.data, g.stride,
+                                     float(scale), out.data_ptr(), workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), _on()))
     return out
 
 
@@ -139,40 +158,46 @@ class IrrepsNorm:
             self._h = None
 
     def _w(self, t, name):
+        if t is None:
+            return None
         _need(t, name, self.wdtype, (self.channels,))
-        return _ptr(t)
+        return t.data_ptr()
 
-    def _in(self, t, name, n, width=None):
-        return _rows(t, name, self.dtype, (n, self.dim if width is None else width))
+    def _in(self, t, name, n):
+        return _rows(t, name, self.dtype, n, self.dim)
 
-    def _new(self, like, width=None):
-        return torch.empty(like.shape[0], self.dim if width is None else width, dtype=self.dtype,
-                           device=like.device)
+    def _new(self, like, n, width):
+        """New rows, and their description."""
+        t = torch.empty((n, width), dtype=self.dtype, device=like.device)
+        return t, _Rows(t.data_ptr(), width)
 
-    def _new_w(self, like, need):
-        return torch.empty(self.channels, dtype=self.wdtype, device=like.device) if need else None
+    def _space(self, workspace, device):
+        if workspace is None:
+            workspace = _scratch(self.workspace_bytes, device)
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
     def forward(self, x, weight=None, out=None):
         """y = norm(x)."""
         n = x.shape[0]
         xr = self._in(x, "x", n)
         if out is None:
-            out = self._new(x)
-        _check(lib().cgtp_norm_forward(self._h, n, xr, self._w(weight, "weight"),
-                                       self._in(out, "out", n), _stream()))
+            out, o = self._new(x, n, self.dim)
+        else:
+            o = self._in(out, "out", n)
+        _check(lib().cgtp_norm_forward(self._h, n, xr, self._w(weight, "weight"), o, _on()))
         return out
 
     def backward(self, x, grad_out, weight=None, need=(True, True), workspace=None):
         """(grad_x, grad_weight); an entry is None where ``need`` is False."""
         n = x.shape[0]
         xr, gr = self._in(x, "x", n), self._in(grad_out, "grad_out", n)
-        gx = self._new(x) if need[0] else None
-        gw = self._new_w(x, need[1])
-        if gw is not None and workspace is None:
-            workspace = _scratch(self.workspace_bytes, x.device)
-        _check(lib().cgtp_norm_backward(
-            self._h, n, xr, self._w(weight, "weight"), gr, self._in(gx, "grad_x", n), _ptr(gw),
-            _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream()))
+        w = self._w(weight, "weight")
+        gx, o = self._new(x, n, self.dim) if need[0] else (None, _NONE)
+        gw, ws, nws = None, None, 0
+        if need[1]:
+            gw = torch.empty(self.channels, dtype=self.wdtype, device=x.device)
+            workspace, ws, nws = self._space(workspace, x.device)
+        _check(lib().cgtp_norm_backward(self._h, n, xr, w, gr, o, _at(gw), ws, nws, _on()))
         return gx, gw
 
     def residual_forward(self, x, b, weight=None, gate=None, scale=None, next_weight=None,
@@ -181,12 +206,17 @@ class IrrepsNorm:
         ``norm_next`` is False (then None), its norm.  ``out``: (h, y) to write;
         h may be x or b."""
         n = b.shape[0]
-        h, y = out if out is not None else (self._new(b), self._new(b) if norm_next else None)
+        br, xr = self._in(b, "b", n), self._in(x, "x", n)
+        if out is None:
+            h, hr = self._new(b, n, self.dim)
+            y, yr = self._new(b, n, self.dim) if norm_next else (None, _NONE)
+        else:
+            h, y = out
+            hr, yr = self._in(h, "h", n), self._in(y, "y", n)
         _check(lib().cgtp_residual_forward(
-            self._h, n, self._in(x, "x", n), self._in(b, "b", n), self._w(weight, "weight"),
-            self._in(gate, "gate", n, self.channels), self._w(scale, "scale"),
-            self._w(next_weight, "next_weight"), self._in(h, "h", n), self._in(y, "y", n),
-            _stream()))
+            self._h, n, xr, br, self._w(weight, "weight"),
+            _rows(gate, "gate", self.dtype, n, self.channels), self._w(scale, "scale"),
+            self._w(next_weight, "next_weight"), hr, yr, _on()))
         return h, y
 
     def residual_backward(self, b, h, grad_h, grad_y=None, weight=None, gate=None, scale=None,
@@ -194,24 +224,27 @@ class IrrepsNorm:
         """(grad_x, grad_b, grad_gate, grad_weight, grad_scale, grad_next_weight)
         for the cotangents of residual_forward's h and y (either may be None);
         ``h`` as it returned it (None without grad_y).  Entries not in ``need``
-        and those of absent arguments (gate) are None."""
+        and those of absent arguments (gate; next_weight without grad_y) are
+        None."""
         n = b.shape[0]
-        rows = [self._in(t, name, n) for t, name in
-                ((b, "b"), (h, "h"), (grad_h, "grad_h"), (grad_y, "grad_y"))]
-        gx = self._new(b) if need[0] else None
-        gb = self._new(b) if need[1] else None
-        gz = self._new(b, self.channels) if need[2] and gate is not None else None
-        gw, gs = self._new_w(b, need[3]), self._new_w(b, need[4])
-        gn = self._new_w(b, need[5] and grad_y is not None)
-        if (gw is not None or gs is not None or gn is not None) and workspace is None:
-            workspace = _scratch(self.workspace_bytes, b.device)
+        br, hr = self._in(b, "b", n), self._in(h, "h", n)
+        ghr, gyr = self._in(grad_h, "grad_h", n), self._in(grad_y, "grad_y", n)
+        zr = _rows(gate, "gate", self.dtype, n, self.channels)
+        none = (None, _NONE)
+        gx, gxr = self._new(b, n, self.dim) if need[0] else none
+        gb, gbr = self._new(b, n, self.dim) if need[1] else none
+        gz, gzr = self._new(b, n, self.channels) if need[2] and gate is not None else none
+        sums = [need[3], need[4], need[5] and grad_y is not None]
+        gw = gs = gn = ws = None
+        nws = 0
+        if any(sums):
+            gw, gs, gn = (torch.empty(self.channels, dtype=self.wdtype, device=b.device)
+                          if wanted else None for wanted in sums)
+            workspace, ws, nws = self._space(workspace, b.device)
         _check(lib().cgtp_residual_backward(
-            self._h, n, rows[0], rows[1], self._w(weight, "weight"),
-            self._in(gate, "gate", n, self.channels), self._w(scale, "scale"),
-            self._w(next_weight, "next_weight"), rows[2], rows[3], self._in(gx, "grad_x", n),
-            self._in(gb, "grad_b", n), self._in(gz, "grad_gate", n, self.channels), _ptr(gw),
-            _ptr(gs), _ptr(gn), _ptr(workspace), 0 if workspace is None else workspace.numel(),
-            _stream()))
+            self._h, n, br, hr, self._w(weight, "weight"), zr, self._w(scale, "scale"),
+            self._w(next_weight, "next_weight"), ghr, gyr, gxr, gbr, gzr, _at(gw), _at(gs),
+            _at(gn), ws, nws, _on()))
         return gx, gb, gz, gw, gs, gn
 
 
@@ -248,7 +281,11 @@ class AdamW:
         self.weight_decay, self.state_bits, self.seed = float(weight_decay), state_bits, int(seed)
         self.step_count = 0
         n = len(self.params)
-        numel = (ctypes.c_int64 * n)(*[p.numel() for p in self.params])
+        # cgtp_adamw_tensor rows: parameter, gradient, length; filled in by step()
+        self._table = np.zeros((n, 3), dtype=np.int64)
+        self._shapes = [p.shape for p in self.params]
+        self._table[:, 2] = [p.numel() for p in self.params]
+        numel = (ctypes.c_int64 * n)(*self._table[:, 2].tolist())
         first, total = (ctypes.c_int64 * n)(), ctypes.c_int64()
         _check(lib().cgtp_adamw_layout(n, numel, first, ctypes.byref(total)))
         self.first, self.total = list(first), total.value
@@ -272,20 +309,21 @@ class AdamW:
         replaces the rate for this step."""
         if len(grads) != len(self.params):
             raise CgtpError(f"{len(grads)} gradients for {len(self.params)} parameters")
-        gtype = grads[0].dtype
-        table = (_AdamwTensor * len(grads))()
-        for t, p, g in zip(table, self.params, grads):
-            if g.dtype != gtype or g.shape != p.shape or not g.is_cuda or not g.is_contiguous():
-                raise CgtpError(f"a gradient is {g.dtype} {tuple(g.shape)} on {g.device}"
-                                f"{'' if g.is_contiguous() else ', not contiguous'}; expected "
-                                f"contiguous {gtype} {tuple(p.shape)}")
-            t.param, t.grad, t.numel = p.data_ptr(), g.data_ptr(), p.numel()
+        gtype, table, params = grads[0].dtype, self._table, self.params
+        for what, tensors, dtype in (("gradient", grads, gtype), ("parameter", params, self.dtype)):
+            if not ([t.shape for t in tensors] == self._shapes
+                    and {t.dtype for t in tensors} == {dtype}
+                    and all(t.is_cuda and t.is_contiguous() for t in tensors)):
+                raise CgtpError(f"the {what}s must be contiguous CUDA tensors of {dtype} with the "
+                                "shapes that the parameters were given with")
+        table[:, 0] = [p.data_ptr() for p in params]
+        table[:, 1] = [g.data_ptr() for g in grads]
         args = _AdamwArgs(self.lr if lr is None else float(lr), *self.betas, self.eps,
                           self.weight_decay, self.step_count + 1, self.seed)
         _check(lib().cgtp_adamw_step(_type(self.dtype), _type(gtype), self.state_bits, len(grads),
-                                     table, _ptr(self.m), _ptr(self.v), _ptr(self.m_exp),
-                                     _ptr(self.v_exp), _ptr(self.copy), self._copy_type,
-                                     ctypes.byref(args), _stream()))
+                                     table.ctypes.data, self.m.data_ptr(), self.v.data_ptr(),
+                                     _at(self.m_exp), _at(self.v_exp), _at(self.copy),
+                                     self._copy_type, ctypes.byref(args), _on()))
         self.step_count += 1
 
     def state_values(self, dtype=torch.bfloat16):
@@ -294,7 +332,7 @@ class AdamW:
         if self.state_bits != 8:
             raise CgtpError("state_values() is for 8-bit states")
         m, v = (torch.empty(self.total, dtype=dtype, device=self.device) for _ in range(2))
-        _check(lib().cgtp_adamw_values(self.total, _ptr(self.m), _ptr(self.m_exp), _ptr(self.v),
-                                       _ptr(self.v_exp), _type(dtype), _ptr(m), _ptr(v),
-                                       _stream()))
+        _check(lib().cgtp_adamw_values(self.total, self.m.data_ptr(), self.m_exp.data_ptr(),
+                                       self.v.data_ptr(), self.v_exp.data_ptr(), _type(dtype),
+                                       m.data_ptr(), v.data_ptr(), _on()))
         return m, v
