@@ -70,32 +70,44 @@ __device__ __forceinline__ float block_scale(uint32_t byte) {
     return __uint_as_float(byte == 255u ? 0x7FC00000u : b);
 }
 
-// Exponent byte of a block whose largest magnitude has the given fp32 bits.
+// x shifted left (right where by < 0).
+__device__ __forceinline__ uint32_t shifted(uint32_t x, int by) {
+    return by >= 0 ? x << by : x >> -by;
+}
+
+// Exponent of a block whose largest magnitude has the given fp32 bits.
 __device__ __forceinline__ int block_exponent(uint32_t top) {
     return min(max((int)(top >> 23) - 126, -80), 126);
 }
 
-// sign, 4 exponent, 3 fraction bits; the exponent field of 2^111 times the
-// value is the code's own, so encoding is a shift of the fp32 bits.
-__device__ __forceinline__ float decode_m(uint32_t c, float scale) {
-    const float a = __uint_as_float((c & 0x7Fu) << 20) * 0x1p111f * scale;
-    return __uint_as_float(__float_as_uint(a) | (c & 0x80u) << 24);
+// m: sign, 4 exponent, 3 fraction bits.  The exponent field of 2^-111 times the
+// value over the block's power of two is the code's own, so encoding is a shift
+// of the fp32 bits, and decoding the shift back; both products are exact but for
+// what lies below the code's last bit.
+__device__ __forceinline__ Two<float> decode_m(uint32_t four, int i, Two<float> scale) {
+    auto magnitude = [&](int k) { return __uint_as_float(shifted(four, 20 - 8 * k) & 0x07F00000u); };
+    auto sign = [&](int k) { return shifted(four, 24 - 8 * k) & 0x80000000u; };
+    Two<float> a{magnitude(i), magnitude(i + 1)};
+    a = a * Two<float>{0x1p111f, 0x1p111f} * scale;
+    return {__uint_as_float(__float_as_uint(a.x) | sign(i)),
+            __uint_as_float(__float_as_uint(a.y) | sign(i + 1))};
 }
-__device__ __forceinline__ uint32_t encode_m(float x, float inv, uint32_t noise) {
-    const uint32_t y = __float_as_uint(__fmul_rn(__fmul_rn(fabsf(x), inv), 0x1p-111f));
-    return min((y + noise) >> 20, 127u) | (__float_as_uint(x) >> 24 & 0x80u);
+__device__ __forceinline__ uint32_t code_m(float y, float x, uint32_t noise) {
+    return min((__float_as_uint(y) + noise) >> 20, 127u) | (__float_as_uint(x) >> 24 & 0x80u);
 }
-__device__ __forceinline__ float decode_v(uint32_t c, float scale) {
-    return __uint_as_float(c << 20) * 0x1p95f * scale;
+// v: 5 exponent and 3 fraction bits, no sign.
+__device__ __forceinline__ Two<float> decode_v(uint32_t four, int i, Two<float> scale) {
+    auto value = [&](int k) { return __uint_as_float(shifted(four, 20 - 8 * k) & 0x0FF00000u); };
+    return Two<float>{value(i), value(i + 1)} * Two<float>{0x1p95f, 0x1p95f} * scale;
 }
-__device__ __forceinline__ uint32_t encode_v(float x, float inv, uint32_t noise) {
-    const uint32_t y = __float_as_uint(__fmul_rn(__fmul_rn(x, inv), 0x1p-95f));
-    return max(min((y + noise) >> 20, 255u), x > 0.f ? 1u : 0u);
+__device__ __forceinline__ uint32_t code_v(float y, float x, uint32_t noise) {
+    return max(min((__float_as_uint(y) + noise) >> 20, 255u), x > 0.f ? 1u : 0u);
 }
 
 // The moments' recursions keep their two products apart (no fused multiply-add):
 // the stochastic rounding that follows compares against exact thresholds, and
-// this is the form that other implementations reproduce bit for bit.
+// this is the form that other implementations reproduce bit for bit.  One value
+// at a time: the packed instructions are contracted even where .rn is written.
 __device__ __forceinline__ float ema(float s, float b, float x, float c) {
     return __fadd_rn(__fmul_rn(s, b), __fmul_rn(x, c));
 }
@@ -108,9 +120,10 @@ __device__ __forceinline__ double square(double x) { return __dmul_rn(x, x); }
 // The step itself needs no exact rounding: a few units in the last place of
 // m / sqrt(v) move p by lr times that.
 __device__ __forceinline__ float stepped(float p, float m, float v, const AdamwScalars<float>& a) {
-    float r;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return p * a.keep - a.rate * __fdividef(m, r * a.root + a.eps);
+    float r, q;  // a subnormal v's root is far below eps
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(r * a.root + a.eps));
+    return p * a.keep - a.rate * (m * q);
 }
 __device__ __forceinline__ double stepped(double p, double m, double v,
                                           const AdamwScalars<double>& a) {
@@ -127,6 +140,7 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
     using C = typename Compute<P>::type;
     constexpr int V = sizeof(C) == 8 ? 2 : 4;  // elements of one access
     constexpr int NV = kBlock / 32 / V;        // accesses of a lane
+    constexpr int H = V / 2;
     const int lane = threadIdx.x & 31;
     const uint32_t warps = gridDim.x * kWarps;
     for (uint32_t b = blockIdx.x * kWarps + (threadIdx.x >> 5); b < tab.blocks; b += warps) {
@@ -146,7 +160,8 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
         const int64_t at = (int64_t)b * kBlock;
         const bool whole = left >= kBlock && (uintptr_t)p % (sizeof(P) * V) == 0 &&
                            (uintptr_t)g % (sizeof(G) * V) == 0;
-        C pn[NV][V], gg[NV][V], m[NV][V], v[NV][V];
+        C pn[NV][V], gg[NV][V];
+        Two<C> m[NV][H], v[NV][H];
         if (whole) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
@@ -173,9 +188,9 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
                 const uint32_t mc = *reinterpret_cast<const uint32_t*>((uint8_t*)m_ + k);
                 const uint32_t vc = *reinterpret_cast<const uint32_t*>((uint8_t*)v_ + k);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    m[j][i] = decode_m(mc >> 8 * i & 0xFFu, ms);
-                    v[j][i] = decode_v(vc >> 8 * i & 0xFFu, vs);
+                for (int i = 0; i < H; ++i) {
+                    m[j][i] = decode_m(mc, 2 * i, {ms, ms});
+                    v[j][i] = decode_v(vc, 2 * i, {vs, vs});
                 }
             }
         } else {
@@ -184,20 +199,25 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
                 const int64_t k = at + (j * 32 + lane) * V;
                 const Pack<C, V> mp = load_pack<C, V>((C*)m_ + k), vp = load_pack<C, V>((C*)v_ + k);
 #pragma unroll
-                for (int i = 0; i < V; ++i) m[j][i] = mp.get(i), v[j][i] = vp.get(i);
+                for (int i = 0; i < H; ++i) m[j][i] = two_at(mp, i), v[j][i] = two_at(vp, i);
             }
         }
         uint32_t mtop = 0, vtop = 0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                m[j][i] = ema(m[j][i], a.b1, gg[j][i], a.c1);
-                v[j][i] = ema(v[j][i], a.b2, square(gg[j][i]), a.c2);
-                pn[j][i] = stepped(pn[j][i], m[j][i], v[j][i], a);
+            for (int i = 0; i < H; ++i) {
+                const C g0 = gg[j][2 * i], g1 = gg[j][2 * i + 1];
+                const Two<C> mm = m[j][i] = {ema(m[j][i].x, a.b1, g0, a.c1),
+                                             ema(m[j][i].y, a.b1, g1, a.c1)};
+                const Two<C> vv = v[j][i] = {ema(v[j][i].x, a.b2, square(g0), a.c2),
+                                             ema(v[j][i].y, a.b2, square(g1), a.c2)};
+                pn[j][2 * i] = stepped(pn[j][2 * i], mm.x, vv.x, a);
+                pn[j][2 * i + 1] = stepped(pn[j][2 * i + 1], mm.y, vv.y, a);
                 if constexpr (EIGHT) {
-                    mtop = max(mtop, __float_as_uint(m[j][i]) & 0x7FFFFFFFu);
-                    vtop = max(vtop, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
+                    mtop = max(mtop, max(__float_as_uint(mm.x) & 0x7FFFFFFFu,
+                                         __float_as_uint(mm.y) & 0x7FFFFFFFu));
+                    vtop = max(vtop, max(__float_as_uint(vv.x), __float_as_uint(vv.y)));
                 }
             }
         }
@@ -244,15 +264,22 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
             const float mi = __uint_as_float((uint32_t)(127 - me) << 23);
             const float vi = __uint_as_float((uint32_t)(127 - ve) << 23);
             const uint32_t key = mix32(e.key + (uint32_t)((uint64_t)first >> 32));
+            const Two<float> mi2{mi, mi}, vi2{vi, vi};
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 uint32_t mc = 0, vc = 0;
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const uint32_t k = (uint32_t)first + (j * 32 + lane) * V + i;
-                    const uint32_t h = mix32(k ^ key);
-                    mc |= encode_m(m[j][i], mi, (h >> 16 << 4) + 8u) << 8 * i;
-                    vc |= encode_v(v[j][i], vi, ((h & 0xFFFFu) << 4) + 8u) << 8 * i;
+                for (int i = 0; i < H; ++i) {
+                    const Two<float> x = m[j][i], y = v[j][i];
+                    const Two<float> ym =
+                        Two<float>{fabsf(x.x), fabsf(x.y)} * mi2 * Two<float>{0x1p-111f, 0x1p-111f};
+                    const Two<float> yv = y * vi2 * Two<float>{0x1p-95f, 0x1p-95f};
+                    const uint32_t k = (uint32_t)first + (j * 32 + lane) * V + 2 * i;
+                    const uint32_t h0 = mix32(k ^ key), h1 = mix32((k + 1) ^ key);
+                    auto high = [](uint32_t h) { return (h >> 12 & 0xFFFF0u) | 8u; };
+                    auto low = [](uint32_t h) { return (h << 4 & 0xFFFF0u) | 8u; };
+                    mc |= (code_m(ym.x, x.x, high(h0)) | code_m(ym.y, x.y, high(h1)) << 8) << 16 * i;
+                    vc |= (code_v(yv.x, y.x, low(h0)) | code_v(yv.y, y.y, low(h1)) << 8) << 16 * i;
                 }
                 const int64_t k = at + (j * 32 + lane) * V;
                 *reinterpret_cast<uint32_t*>((uint8_t*)m_ + k) = mc;
@@ -267,8 +294,8 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
             for (int j = 0; j < NV; ++j) {
                 const int64_t k = at + (j * 32 + lane) * V;
                 Pack<C, V> mp, vp;
-                mp.set(m[j]);
-                vp.set(v[j]);
+                set_twos(mp, m[j]);
+                set_twos(vp, v[j]);
                 store_pack((C*)m_ + k, mp);
                 store_pack((C*)v_ + k, vp);
             }
@@ -287,15 +314,12 @@ adamw_values_kernel(int64_t quads, const uint32_t* __restrict__ mc,
          q += (int64_t)gridDim.x * 256) {
         const float ms = block_scale(me[q / (kBlock / 4)]), vs = block_scale(ve[q / (kBlock / 4)]);
         const uint32_t a = mc[q], b = vc[q];
-        float xm[4], xv[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            xm[i] = decode_m(a >> 8 * i & 0xFFu, ms);
-            xv[i] = decode_v(b >> 8 * i & 0xFFu, vs);
-        }
+        const Two<float> m2{ms, ms}, v2{vs, vs};
+        const Two<float> xm[2] = {decode_m(a, 0, m2), decode_m(a, 2, m2)};
+        const Two<float> xv[2] = {decode_v(b, 0, v2), decode_v(b, 2, v2)};
         Pack<O, 4> pm, pv;
-        pm.set(xm);
-        pv.set(xv);
+        set_twos(pm, xm);
+        set_twos(pv, xv);
         store_pack(m + 4 * q, pm);
         store_pack(v + 4 * q, pv);
     }

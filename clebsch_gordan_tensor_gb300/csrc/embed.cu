@@ -25,32 +25,43 @@ namespace {
 
 // ------------------------------------------------------------- lookup --
 
-// A group of T lanes copies a tile of T * V columns of one row.
+// A group of T lanes copies a tile of T * V columns of four rows at a time.
 template <typename S, typename I, int V>
 __global__ void __launch_bounds__(256)
-embed_forward_kernel(int64_t n, int64_t v, int64_t d, int T, int64_t tiles,
+embed_forward_kernel(int64_t n, int64_t v, int64_t d, int T, uint32_t tiles,
                      const I* __restrict__ index, const S* __restrict__ table,
                      typename Compute<S>::type scale, S* __restrict__ out, int64_t stride) {
-    const int64_t groups = (int64_t)gridDim.x * (256 / T);
+    using C = typename Compute<S>::type;
+    constexpr int U = 4;
+    const int64_t items = n * tiles, groups = (int64_t)gridDim.x * (256 / T);
     const int t = threadIdx.x % T;
-    for (int64_t w = (int64_t)blockIdx.x * (256 / T) + threadIdx.x / T; w < n * tiles;
-         w += groups) {
-        const int64_t row = w / tiles, col = (w % tiles * T + t) * V;
-        if (col >= d) continue;
-        const int64_t i = index[row];
-        Pack<S, V> p;
-        typename Compute<S>::type x[V];
-        if (i >= 0 && i < v) {
-            p = load_pack<S, V>(table + i * d + col);
+    for (int64_t w = (int64_t)blockIdx.x * (256 / T) + threadIdx.x / T; w < items;
+         w += U * groups) {
+        int64_t row[U], col[U], from[U];
 #pragma unroll
-            for (int k = 0; k < V; ++k) x[k] = p.get(k) * scale;
-        } else {
-            if (i >= v && t == 0) cgtp_embed_error = 1;
-#pragma unroll
-            for (int k = 0; k < V; ++k) x[k] = 0;
+        for (int u = 0; u < U; ++u) {
+            const int64_t item = w + u * groups;
+            row[u] = tiles == 1 ? item : item / tiles;
+            col[u] = ((item - row[u] * tiles) * T + t) * V;
+            from[u] = item < items && col[u] < d ? (int64_t)index[row[u]] : -2;
         }
-        p.set(x);
-        store_pack(out + row * stride + col, p);
+        Pack<S, V> p[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            p[u].fill((C)0);
+            if (from[u] >= 0 && from[u] < v) p[u] = load_pack<S, V>(table + from[u] * d + col[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (w + u * groups >= items || col[u] >= d) continue;
+            if (from[u] >= v && t == 0) cgtp_embed_error = 1;
+            C x[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                x[k] = from[u] >= 0 && from[u] < v ? p[u].get(k) * scale : (C)0;
+            p[u].set(x);
+            stream_pack(out + row[u] * stride + col[u], p[u]);
+        }
     }
 }
 
@@ -566,9 +577,9 @@ template <typename S, typename I, int V>
 cudaError_t forward_v(const EmbedCall& c, cudaStream_t s) {
     using C = typename Compute<S>::type;
     const int T = lanes_for((c.d + V - 1) / V);
-    const int64_t tiles = (c.d + (int64_t)T * V - 1) / ((int64_t)T * V);
+    const uint32_t tiles = (uint32_t)((c.d + (int64_t)T * V - 1) / ((int64_t)T * V));
     const unsigned grid =
-        (unsigned)std::min<int64_t>((c.n * tiles + 256 / T - 1) / (256 / T), 152 * 64);
+        (unsigned)std::min<int64_t>((c.n * tiles + 256 / T - 1) / (256 / T), 152 * 16);
     embed_forward_kernel<S, I, V><<<grid, 256, 0, s>>>(
         c.n, c.v, c.d, T, tiles, (const I*)c.index, (const S*)c.in, (C)c.scale, (S*)c.out,
         c.out_stride);

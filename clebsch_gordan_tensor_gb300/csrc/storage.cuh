@@ -101,6 +101,15 @@ __device__ __forceinline__ void store_pack(S* p, const Pack<S, V>& x) {
     *reinterpret_cast<Pack<S, V>*>(p) = x;
 }
 
+// A store that the caches need not keep.
+template <typename S, int V>
+__device__ __forceinline__ void stream_pack(S* p, const Pack<S, V>& x) {
+    if constexpr (sizeof(S) * V == 16)
+        __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&x));
+    else
+        store_pack(p, x);
+}
+
 // Two values that go through the arithmetic together: one packed instruction
 // for each pair of fp32 operations.
 template <typename C>
