@@ -95,6 +95,12 @@ __device__ __forceinline__ Two<float> decode_m(uint32_t four, int i, Two<float> 
 __device__ __forceinline__ uint32_t code_m(float y, float x, uint32_t noise) {
     return min((__float_as_uint(y) + noise) >> 20, 127u) | (__float_as_uint(x) >> 24 & 0x80u);
 }
+// The larger magnitude, NaN if either is.
+__device__ __forceinline__ float larger(float top, float x) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(top), "f"(fabsf(x)));
+    return r;
+}
 // v: 5 exponent and 3 fraction bits, no sign.
 __device__ __forceinline__ Two<float> decode_v(uint32_t four, int i, Two<float> scale) {
     auto value = [&](int k) { return __uint_as_float(shifted(four, 20 - 8 * k) & 0x0FF00000u); };
@@ -132,7 +138,7 @@ __device__ __forceinline__ double stepped(double p, double m, double v,
 
 // copy_kind: 0 none, 1 bfloat16, 2 binary16.
 template <typename P, typename G, bool EIGHT>
-__global__ void __launch_bounds__(32 * kWarps)
+__global__ void __launch_bounds__(32 * kWarps, EIGHT ? 5 : 1)
 adamw_kernel(const __grid_constant__ AdamwTable tab,
              const AdamwScalars<typename Compute<P>::type> a, void* __restrict__ m_,
              void* __restrict__ v_, uint8_t* __restrict__ m_exp, uint8_t* __restrict__ v_exp,
@@ -143,15 +149,9 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
     constexpr int H = V / 2;
     const int lane = threadIdx.x & 31;
     const uint32_t warps = gridDim.x * kWarps;
+    int lo = 0;  // the block's tensor: the last one that starts at or before it
     for (uint32_t b = blockIdx.x * kWarps + (threadIdx.x >> 5); b < tab.blocks; b += warps) {
-        int lo = 0, hi = tab.n - 1;  // the last tensor that starts at or before block b
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (tab.t[mid].block0 <= b)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
+        while (lo + 1 < tab.n && tab.t[lo + 1].block0 <= b) ++lo;
         const AdamwEntry& e = tab.t[lo];
         const int64_t first = (int64_t)(b - e.block0) * kBlock;
         P* p = static_cast<P*>(e.p) + first;
@@ -202,7 +202,7 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
                 for (int i = 0; i < H; ++i) m[j][i] = two_at(mp, i), v[j][i] = two_at(vp, i);
             }
         }
-        uint32_t mtop = 0, vtop = 0;
+        float mbig = 0.f, vbig = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
 #pragma unroll
@@ -215,9 +215,8 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
                 pn[j][2 * i] = stepped(pn[j][2 * i], mm.x, vv.x, a);
                 pn[j][2 * i + 1] = stepped(pn[j][2 * i + 1], mm.y, vv.y, a);
                 if constexpr (EIGHT) {
-                    mtop = max(mtop, max(__float_as_uint(mm.x) & 0x7FFFFFFFu,
-                                         __float_as_uint(mm.y) & 0x7FFFFFFFu));
-                    vtop = max(vtop, max(__float_as_uint(vv.x), __float_as_uint(vv.y)));
+                    mbig = larger(larger(mbig, mm.x), mm.y);
+                    vbig = larger(larger(vbig, vv.x), vv.y);
                 }
             }
         }
@@ -258,8 +257,9 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
             }
         }
         if constexpr (EIGHT) {
-            mtop = __reduce_max_sync(0xFFFFFFFFu, mtop);
-            vtop = __reduce_max_sync(0xFFFFFFFFu, vtop);
+            // as bits, in which infinity and NaN are above every number
+            const uint32_t mtop = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mbig));
+            const uint32_t vtop = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(vbig));
             const int me = block_exponent(mtop), ve = block_exponent(vtop);
             const float mi = __uint_as_float((uint32_t)(127 - me) << 23);
             const float vi = __uint_as_float((uint32_t)(127 - ve) << 23);
@@ -335,8 +335,8 @@ cudaError_t launch(const AdamwTable& tab, const AdamwCall& c, int64_t block0, cu
                             (C)(1.0 / std::sqrt(bc2)), (C)c.eps};
     const size_t each = EIGHT ? 1 : sizeof(C);
     const int64_t at = block0 * kBlock;
-    const unsigned grid =
-        (unsigned)std::min<int64_t>(((int64_t)tab.blocks + kWarps - 1) / kWarps, 152 * 8);
+    const int64_t ctas = ((int64_t)tab.blocks + kWarps - 1) / kWarps;
+    const unsigned grid = (unsigned)std::min<int64_t>(ctas, 152 * 8);
     adamw_kernel<P, G, EIGHT><<<grid, 32 * kWarps, 0, s>>>(
         tab, a, (uint8_t*)c.m + at * each, (uint8_t*)c.v + at * each,
         EIGHT ? c.m_exp + block0 : nullptr, EIGHT ? c.v_exp + block0 : nullptr,

@@ -25,42 +25,67 @@ namespace {
 
 // ------------------------------------------------------------- lookup --
 
-// A group of T lanes copies a tile of T * V columns of four rows at a time.
-template <typename S, typename I, int V>
+// A group of T lanes copies R = 4 vectors a lane at a time: of four rows where a
+// row fits the lanes (Long false), of one row where it does not.  No division:
+// with a tile number computed for every vector the copy of 131,072 x 1024 bf16
+// rows was bound by its instructions (74 us).
+template <typename S, typename I, int V, bool Long>
 __global__ void __launch_bounds__(256)
-embed_forward_kernel(int64_t n, int64_t v, int64_t d, int T, uint32_t tiles,
-                     const I* __restrict__ index, const S* __restrict__ table,
-                     typename Compute<S>::type scale, S* __restrict__ out, int64_t stride) {
+embed_forward_kernel(int64_t n, int64_t v, int64_t d, int T, const I* __restrict__ index,
+                     const S* __restrict__ table, typename Compute<S>::type scale,
+                     S* __restrict__ out, int64_t stride) {
     using C = typename Compute<S>::type;
-    constexpr int U = 4;
-    const int64_t items = n * tiles, groups = (int64_t)gridDim.x * (256 / T);
-    const int t = threadIdx.x % T;
-    for (int64_t w = (int64_t)blockIdx.x * (256 / T) + threadIdx.x / T; w < items;
-         w += U * groups) {
-        int64_t row[U], col[U], from[U];
+    constexpr int R = 4;
+    const int64_t groups = (int64_t)gridDim.x * (256 / T);
+    const int64_t group = (int64_t)blockIdx.x * (256 / T) + threadIdx.x / T;
+    const int col0 = threadIdx.x % T * V;
+    auto scaled = [&](Pack<S, V>& p) {
+        C x[V];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t item = w + u * groups;
-            row[u] = tiles == 1 ? item : item / tiles;
-            col[u] = ((item - row[u] * tiles) * T + t) * V;
-            from[u] = item < items && col[u] < d ? (int64_t)index[row[u]] : -2;
+        for (int k = 0; k < V; ++k) x[k] = p.get(k) * scale;
+        p.set(x);
+    };
+    if constexpr (Long) {
+        for (int64_t row = group; row < n; row += groups) {
+            const int64_t i = index[row];
+            const bool named = i >= 0 && i < v;
+            if (i >= v && col0 == 0) cgtp_embed_error = 1;
+            const S* from = table + (named ? i : 0) * d;
+            S* to = out + row * stride;
+            for (int64_t col = col0; col < d; col += R * T * V) {
+                Pack<S, V> p[R];
+#pragma unroll
+                for (int u = 0; u < R; ++u) {
+                    p[u].fill((C)0);
+                    if (named && col + u * T * V < d) p[u] = load_pack<S, V>(from + col + u * T * V);
+                }
+#pragma unroll
+                for (int u = 0; u < R; ++u)
+                    if (col + u * T * V < d) {
+                        if (named) scaled(p[u]);
+                        stream_pack(to + col + u * T * V, p[u]);
+                    }
+            }
         }
-        Pack<S, V> p[U];
+    } else {
+        if (col0 >= d) return;
+        for (int64_t row = group * R; row < n; row += groups * R) {
+            int64_t i[R];
+            Pack<S, V> p[R];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            p[u].fill((C)0);
-            if (from[u] >= 0 && from[u] < v) p[u] = load_pack<S, V>(table + from[u] * d + col[u]);
-        }
+            for (int u = 0; u < R; ++u) i[u] = row + u < n ? (int64_t)index[row + u] : -1;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (w + u * groups >= items || col[u] >= d) continue;
-            if (from[u] >= v && t == 0) cgtp_embed_error = 1;
-            C x[V];
+            for (int u = 0; u < R; ++u) {
+                p[u].fill((C)0);
+                if (i[u] >= 0 && i[u] < v) p[u] = load_pack<S, V>(table + i[u] * d + col0);
+            }
 #pragma unroll
-            for (int k = 0; k < V; ++k)
-                x[k] = from[u] >= 0 && from[u] < v ? p[u].get(k) * scale : (C)0;
-            p[u].set(x);
-            stream_pack(out + row[u] * stride + col[u], p[u]);
+            for (int u = 0; u < R; ++u)
+                if (row + u < n) {
+                    if (i[u] >= v && col0 == 0) cgtp_embed_error = 1;
+                    if (i[u] >= 0 && i[u] < v) scaled(p[u]);
+                    stream_pack(out + (row + u) * stride + col0, p[u]);
+                }
         }
     }
 }
@@ -577,12 +602,13 @@ template <typename S, typename I, int V>
 cudaError_t forward_v(const EmbedCall& c, cudaStream_t s) {
     using C = typename Compute<S>::type;
     const int T = lanes_for((c.d + V - 1) / V);
-    const uint32_t tiles = (uint32_t)((c.d + (int64_t)T * V - 1) / ((int64_t)T * V));
-    const unsigned grid =
-        (unsigned)std::min<int64_t>((c.n * tiles + 256 / T - 1) / (256 / T), 152 * 16);
-    embed_forward_kernel<S, I, V><<<grid, 256, 0, s>>>(
-        c.n, c.v, c.d, T, tiles, (const I*)c.index, (const S*)c.in, (C)c.scale, (S*)c.out,
-        c.out_stride);
+    const bool long_rows = c.d > (int64_t)T * V;
+    const int64_t groups = long_rows ? c.n : (c.n + 3) / 4;
+    const unsigned grid = (unsigned)std::min<int64_t>((groups + 256 / T - 1) / (256 / T), 152 * 16);
+    auto kernel = long_rows ? embed_forward_kernel<S, I, V, true>
+                            : embed_forward_kernel<S, I, V, false>;
+    kernel<<<grid, 256, 0, s>>>(c.n, c.v, c.d, T, (const I*)c.index, (const S*)c.in, (C)c.scale,
+                                (S*)c.out, c.out_stride);
     count_launch();
     return cudaGetLastError();
 }
