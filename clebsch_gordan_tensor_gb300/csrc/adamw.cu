@@ -43,6 +43,7 @@ struct AdamwEntry {
     int64_t numel;
     uint32_t block0;  // first block in this launch
     uint32_t key;     // of the rounding hash
+    uint32_t vectors; // whether its addresses allow vector accesses
 };
 
 struct AdamwTable {
@@ -85,29 +86,52 @@ __device__ __forceinline__ int block_exponent(uint32_t top) {
 // of the fp32 bits, and decoding the shift back; both products are exact but for
 // what lies below the code's last bit.
 __device__ __forceinline__ Two<float> decode_m(uint32_t four, int i, Two<float> scale) {
-    auto magnitude = [&](int k) { return __uint_as_float(shifted(four, 20 - 8 * k) & 0x07F00000u); };
-    auto sign = [&](int k) { return shifted(four, 24 - 8 * k) & 0x80000000u; };
-    Two<float> a{magnitude(i), magnitude(i + 1)};
-    a = a * Two<float>{0x1p111f, 0x1p111f} * scale;
-    return {__uint_as_float(__float_as_uint(a.x) | sign(i)),
-            __uint_as_float(__float_as_uint(a.y) | sign(i + 1))};
-}
-__device__ __forceinline__ uint32_t code_m(float y, float x, uint32_t noise) {
-    return min((__float_as_uint(y) + noise) >> 20, 127u) | (__float_as_uint(x) >> 24 & 0x80u);
-}
-// The larger magnitude, NaN if either is.
-__device__ __forceinline__ float larger(float top, float x) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(top), "f"(fabsf(x)));
-    return r;
+    auto value = [&](int k) {  // the byte to the top, and its sign spread by the shift back
+        return __int_as_float((int)(four << (24 - 8 * k)) >> 4 & (int)0x87F00000u);
+    };
+    return Two<float>{value(i), value(i + 1)} * Two<float>{0x1p111f, 0x1p111f} * scale;
 }
 // v: 5 exponent and 3 fraction bits, no sign.
 __device__ __forceinline__ Two<float> decode_v(uint32_t four, int i, Two<float> scale) {
     auto value = [&](int k) { return __uint_as_float(shifted(four, 20 - 8 * k) & 0x0FF00000u); };
     return Two<float>{value(i), value(i + 1)} * Two<float>{0x1p95f, 0x1p95f} * scale;
 }
-__device__ __forceinline__ uint32_t code_v(float y, float x, uint32_t noise) {
-    return max(min((__float_as_uint(y) + noise) >> 20, 255u), x > 0.f ? 1u : 0u);
+// y, the fp32 bits of a scaled magnitude, with the noise below the last bit kept
+// added: the code, but for the clamp at the largest one.
+__device__ __forceinline__ int rounded(float y, uint32_t noise) {
+    return (int)((__float_as_uint(y) + noise) >> 20);
+}
+// Four codes, clamped to a signed (127) or unsigned (255) byte, first one lowest.
+__device__ __forceinline__ uint32_t pack_s8(int a, int b, int c, int d) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 t;\n\t"
+        "cvt.pack.sat.s8.s32.b32 t, %4, %3, 0;\n\t"
+        "cvt.pack.sat.s8.s32.b32 %0, %2, %1, t;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(b), "r"(c), "r"(d));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_u8(int a, int b, int c, int d) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 t;\n\t"
+        "cvt.pack.sat.u8.s32.b32 t, %4, %3, 0;\n\t"
+        "cvt.pack.sat.u8.s32.b32 %0, %2, %1, t;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(b), "r"(c), "r"(d));
+    return r;
+}
+// The sign bits of four values at the bytes' top.
+__device__ __forceinline__ uint32_t signs(Two<float> a, Two<float> b) {
+    const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0073);
+    const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0073);
+    return __byte_perm(lo, hi, 0x5410) & 0x80808080u;
+}
+
+// The larger magnitude, NaN if either is.
+__device__ __forceinline__ float larger(float top, float x) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(top), "f"(fabsf(x)));
+    return r;
 }
 
 // The moments' recursions keep their two products apart (no fused multiply-add):
@@ -125,15 +149,23 @@ __device__ __forceinline__ double square(double x) { return __dmul_rn(x, x); }
 
 // The step itself needs no exact rounding: a few units in the last place of
 // m / sqrt(v) move p by lr times that.
-__device__ __forceinline__ float stepped(float p, float m, float v, const AdamwScalars<float>& a) {
-    float r, q;  // a subnormal v's root is far below eps
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(r * a.root + a.eps));
-    return p * a.keep - a.rate * (m * q);
+__device__ __forceinline__ Two<float> stepped(Two<float> p, Two<float> m, Two<float> v,
+                                              const AdamwScalars<float>& a) {
+    Two<float> r, q;  // a subnormal v's root is far below eps
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(v.x));
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(v.y));
+    r = fma(r, Two<float>{a.root, a.root}, Two<float>{a.eps, a.eps});
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q.x) : "f"(r.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q.y) : "f"(r.y));
+    return fma(p, Two<float>{a.keep, a.keep}, m * q * Two<float>{-a.rate, -a.rate});
 }
 __device__ __forceinline__ double stepped(double p, double m, double v,
                                           const AdamwScalars<double>& a) {
     return p * a.keep - a.rate * (m / (sqrt(v) * a.root + a.eps));
+}
+__device__ __forceinline__ Two<double> stepped(Two<double> p, Two<double> m, Two<double> v,
+                                               const AdamwScalars<double>& a) {
+    return {stepped(p.x, m.x, v.x, a), stepped(p.y, m.y, v.y, a)};
 }
 
 // copy_kind: 0 none, 1 bfloat16, 2 binary16.
@@ -154,12 +186,10 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
         while (lo + 1 < tab.n && tab.t[lo + 1].block0 <= b) ++lo;
         const AdamwEntry& e = tab.t[lo];
         const int64_t first = (int64_t)(b - e.block0) * kBlock;
-        P* p = static_cast<P*>(e.p) + first;
-        const G* g = static_cast<const G*>(e.g) + first;
-        const int64_t left = e.numel - first;
-        const int64_t at = (int64_t)b * kBlock;
-        const bool whole = left >= kBlock && (uintptr_t)p % (sizeof(P) * V) == 0 &&
-                           (uintptr_t)g % (sizeof(G) * V) == 0;
+        const int64_t left = e.numel - first, at = (int64_t)b * kBlock;
+        P* const p = static_cast<P*>(e.p) + first;
+        const G* const g = static_cast<const G*>(e.g) + first;
+        const bool whole = left >= kBlock && e.vectors;
         C pn[NV][V], gg[NV][V];
         Two<C> m[NV][H], v[NV][H];
         if (whole) {
@@ -212,8 +242,9 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
                                              ema(m[j][i].y, a.b1, g1, a.c1)};
                 const Two<C> vv = v[j][i] = {ema(v[j][i].x, a.b2, square(g0), a.c2),
                                              ema(v[j][i].y, a.b2, square(g1), a.c2)};
-                pn[j][2 * i] = stepped(pn[j][2 * i], mm.x, vv.x, a);
-                pn[j][2 * i + 1] = stepped(pn[j][2 * i + 1], mm.y, vv.y, a);
+                const Two<C> pp = stepped(Two<C>{pn[j][2 * i], pn[j][2 * i + 1]}, mm, vv, a);
+                pn[j][2 * i] = pp.x;
+                pn[j][2 * i + 1] = pp.y;
                 if constexpr (EIGHT) {
                     mbig = larger(larger(mbig, mm.x), mm.y);
                     vbig = larger(larger(vbig, vv.x), vv.y);
@@ -267,7 +298,7 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
             const Two<float> mi2{mi, mi}, vi2{vi, vi};
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                uint32_t mc = 0, vc = 0;
+                int mc[V], vc[V];
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     const Two<float> x = m[j][i], y = v[j][i];
@@ -278,12 +309,19 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
                     const uint32_t h0 = mix32(k ^ key), h1 = mix32((k + 1) ^ key);
                     auto high = [](uint32_t h) { return (h >> 12 & 0xFFFF0u) | 8u; };
                     auto low = [](uint32_t h) { return (h << 4 & 0xFFFF0u) | 8u; };
-                    mc |= (code_m(ym.x, x.x, high(h0)) | code_m(ym.y, x.y, high(h1)) << 8) << 16 * i;
-                    vc |= (code_v(yv.x, y.x, low(h0)) | code_v(yv.y, y.y, low(h1)) << 8) << 16 * i;
+                    mc[2 * i] = rounded(ym.x, high(h0));
+                    mc[2 * i + 1] = rounded(ym.y, high(h1));
+                    // a positive v keeps a positive code
+                    vc[2 * i] = max(rounded(yv.x, low(h0)), (int)min(__float_as_uint(y.x), 1u));
+                    vc[2 * i + 1] = max(rounded(yv.y, low(h1)), (int)min(__float_as_uint(y.y), 1u));
                 }
                 const int64_t k = at + (j * 32 + lane) * V;
-                *reinterpret_cast<uint32_t*>((uint8_t*)m_ + k) = mc;
-                *reinterpret_cast<uint32_t*>((uint8_t*)v_ + k) = vc;
+                if constexpr (V == 4) {
+                    *reinterpret_cast<uint32_t*>((uint8_t*)m_ + k) =
+                        pack_s8(mc[0], mc[1], mc[2], mc[3]) | signs(m[j][0], m[j][1]);
+                    *reinterpret_cast<uint32_t*>((uint8_t*)v_ + k) =
+                        pack_u8(vc[0], vc[1], vc[2], vc[3]);
+                }
             }
             if (lane == 0) {
                 m_exp[b] = mtop >= 0x7F800000u ? 255 : (uint8_t)(me + 128);
@@ -325,6 +363,17 @@ adamw_values_kernel(int64_t quads, const uint32_t* __restrict__ mc,
     }
 }
 
+int resident_ctas(const void* kernel) {
+    int each = 0, dev = 0, sms = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&each, kernel, 32 * kWarps, 0) !=
+            cudaSuccess ||
+        cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        each * sms <= 0)
+        return 152 * 4;
+    return each * sms;
+}
+
 template <typename P, typename G, bool EIGHT>
 cudaError_t launch(const AdamwTable& tab, const AdamwCall& c, int64_t block0, cudaStream_t s) {
     using C = typename Compute<P>::type;
@@ -336,7 +385,13 @@ cudaError_t launch(const AdamwTable& tab, const AdamwCall& c, int64_t block0, cu
     const size_t each = EIGHT ? 1 : sizeof(C);
     const int64_t at = block0 * kBlock;
     const int64_t ctas = ((int64_t)tab.blocks + kWarps - 1) / kWarps;
-    const unsigned grid = (unsigned)std::min<int64_t>(ctas, 152 * 8);
+    // 8-bit states are bound by arithmetic as much as by HBM: as many CTAs as are
+    // resident at once, for a last wave that fills 0.6 of the SMs cost a fifth.
+    // With 32-bit ones two and two thirds of a wave measured best (968 us against
+    // 1000 us for 240 M parameters).
+    static const int resident =
+        EIGHT ? resident_ctas((const void*)adamw_kernel<P, G, EIGHT>) : 152 * 8;
+    const unsigned grid = (unsigned)std::min<int64_t>(ctas, resident);
     adamw_kernel<P, G, EIGHT><<<grid, 32 * kWarps, 0, s>>>(
         tab, a, (uint8_t*)c.m + at * each, (uint8_t*)c.v + at * each,
         EIGHT ? c.m_exp + block0 : nullptr, EIGHT ? c.v_exp + block0 : nullptr,
@@ -380,7 +435,9 @@ cudaError_t launch_adamw(const AdamwCall& c, cudaStream_t s) {
             // block numbers of one launch are 32 bits wide
             if (tab.n > 0 && block + nb - block0 > 0x7FFFFFFF) break;
             tab.t[tab.n++] = {c.tensors[i].param, c.tensors[i].grad, c.tensors[i].numel,
-                              (uint32_t)(block - block0), mix32(key + (uint32_t)i)};
+                              (uint32_t)(block - block0), mix32(key + (uint32_t)i),
+                              (uintptr_t)c.tensors[i].param % 16 == 0 &&
+                                  (uintptr_t)c.tensors[i].grad % 16 == 0};
             block += nb;
         }
         if (tab.n == 0) continue;

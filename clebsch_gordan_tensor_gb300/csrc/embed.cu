@@ -454,6 +454,83 @@ embed_join_kernel(uint32_t v, int64_t d, int T, uint32_t tiles, uint32_t chunk, 
     }
 }
 
+// Few indices: one launch and no sort.  A warp takes a row of the table, finds
+// its positions among all of them in order, and adds their rows; a row with many
+// is left to its whole CTA, the warps adding consecutive shares.
+constexpr int kSmallN = 1024;
+
+template <typename S, typename I, int V>
+__global__ void __launch_bounds__(256)
+embed_small_kernel(int n, uint32_t v, int64_t d, const I* __restrict__ index,
+                   const S* __restrict__ g, int64_t stride, typename Compute<S>::type scale,
+                   S* __restrict__ table) {
+    using C = typename Compute<S>::type;
+    constexpr int kMany = 32;
+    __shared__ uint32_t keys[kSmallN];
+    __shared__ uint16_t at[8][kSmallN];
+    __shared__ int found[8];
+    __shared__ C part[8][32 * V];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t col = ((int64_t)blockIdx.y * 32 + lane) * V;
+    for (int i = threadIdx.x; i < n; i += 256) keys[i] = key_of(index[i], v);
+    __syncthreads();
+    const uint32_t r = blockIdx.x * 8 + warp;
+    int count = 0;
+    for (int i = 0; r < v && i < n; i += 32) {
+        const bool hit = i + lane < n && keys[i + lane] == r;
+        const uint32_t hits = __ballot_sync(0xFFFFFFFFu, hit);
+        if (hit) at[warp][count + __popc(hits & ((1u << lane) - 1))] = (uint16_t)(i + lane);
+        count += __popc(hits);
+    }
+    if (lane == 0) found[warp] = count;
+    __syncwarp();
+    auto add = [&](C (&acc)[V], const uint16_t* list, int from, int to) {
+        for (int i = from; i < to; i += 8) {
+            Pack<S, V> x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[j].fill((C)0);
+                if (i + j < to && col < d)
+                    x[j] = load_pack<S, V>(g + (int64_t)list[i + j] * stride + col);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int k = 0; k < V; ++k) acc[k] += x[j].get(k);
+        }
+    };
+    auto write = [&](C (&acc)[V], uint32_t row) {
+        Pack<S, V> o;
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] *= scale;
+        o.set(acc);
+        store_pack(table + (int64_t)row * d + col, o);
+    };
+    if (r < v && count <= kMany) {
+        C acc[V] = {};
+        add(acc, at[warp], 0, count);
+        if (col < d) write(acc, r);
+    }
+    __syncthreads();
+    for (int w = 0; w < 8; ++w) {
+        const int all = found[w];
+        if (all <= kMany) continue;
+        const int share = (all + 7) / 8, from = min(warp * share, all);
+        C acc[V] = {};
+        add(acc, at[w], from, min(from + share, all));
+#pragma unroll
+        for (int k = 0; k < V; ++k) part[warp][lane * V + k] = acc[k];
+        __syncthreads();
+        if (warp == 0 && col < d) {
+            for (int q = 1; q < 8; ++q)
+#pragma unroll
+                for (int k = 0; k < V; ++k) acc[k] += part[q][lane * V + k];
+            write(acc, blockIdx.x * 8 + w);
+        }
+        __syncthreads();
+    }
+}
+
 __global__ void __launch_bounds__(256) embed_zero_kernel(uint8_t* __restrict__ p, int64_t bytes) {
     const int64_t words = bytes / 16, step = (int64_t)gridDim.x * 256;
     const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -568,9 +645,37 @@ bool wide(const EmbedCall& c) {
            (uintptr_t)c.in % 16 == 0 && (uintptr_t)c.out % 16 == 0;
 }
 
+template <typename S, typename I, int V>
+cudaError_t small_v(const EmbedCall& c, cudaStream_t s) {
+    const dim3 grid((unsigned)((c.v + 7) / 8), (unsigned)((c.d + 32 * V - 1) / (32 * V)));
+    embed_small_kernel<S, I, V><<<grid, 256, 0, s>>>(
+        (int)c.n, (uint32_t)c.v, c.d, (const I*)c.index, (const S*)c.in, c.in_stride,
+        (typename Compute<S>::type)c.scale, (S*)c.out);
+    count_launch();
+    return cudaGetLastError();
+}
+
+// Whether the gradient takes one launch, with vectors of V elements: few indices,
+// and not so many rows and tiles of columns that each scans all of them for.
+// The time of that kernel goes by the CTAs times the indices and a constant: up
+// to 5 million it matched the sorted form's or beat it (1024 indices, 119 x 64
+// fp32: 24.0 us and 24.2 us in four launches; 16,000 x 512 bf16: 32.0 and 32.3 us
+// in six; 200 indices, 50,000 x 256 fp32: 31.6 and 39.8 us), at 39 million it lost
+// (1024 indices, 32,000 x 2048 bf16: 215 and 52 us).
+bool small(int64_t n, int64_t v, int64_t d, int64_t V) {
+    const int64_t tiles = (d + 32 * V - 1) / (32 * V);
+    return n <= kSmallN && tiles <= 65535 && (v + 7) / 8 * tiles <= 5000000 / (n + 200);
+}
+
 template <typename S>
 cudaError_t backward(const EmbedCall& c, cudaStream_t s) {
     cudaError_t e;
+    if (c.n > 0 && small(c.n, c.v, c.d, wide<S>(c) ? 16 / sizeof(S) : 1)) {
+        constexpr int V = 16 / sizeof(S);
+        if (c.index_bits == 32)
+            return wide<S>(c) ? small_v<S, int32_t, V>(c, s) : small_v<S, int32_t, 1>(c, s);
+        return wide<S>(c) ? small_v<S, int64_t, V>(c, s) : small_v<S, int64_t, 1>(c, s);
+    }
     if (c.n == 0) {
         const int64_t bytes = c.v * c.d * (int64_t)sizeof(S);
         const unsigned grid = (unsigned)std::min<int64_t>(bytes / 4096 + 1, 152 * 16);
@@ -633,7 +738,8 @@ cudaError_t launch_embed_forward(const EmbedCall& c, cudaStream_t s) {
 }
 
 size_t embed_backward_workspace_bytes(cgtp_dtype type, int64_t n, int64_t v, int64_t d) {
-    return n == 0 ? 0 : layout_of(type, n, v, d).total;
+    // single elements make the most tiles: small with them, small with vectors
+    return n == 0 || small(n, v, d, 1) ? 0 : layout_of(type, n, v, d).total;
 }
 
 cudaError_t launch_embed_backward(const EmbedCall& c, cudaStream_t s) {

@@ -108,23 +108,6 @@ __device__ __forceinline__ S* row_of(const cgtp_rows& q, int64_t row, int at) {
     return q.data ? (S*)q.data + row * q.stride + at : nullptr;
 }
 
-// Asynchronous copies to shared memory of 4, 8 or 16 bytes.
-template <int N>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-    if constexpr (N == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N)
-                     : "memory");
-}
-__device__ __forceinline__ void copies_end_group() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // ------------------------------------------------------------- forward --
 
 template <typename S, int V, int L, int K>
@@ -442,7 +425,7 @@ struct BackwardRing {
             const S *gy = row_of<const S>(a.grad_y, row, ir.off);
             const S* z = row_of<const S>(a.gate, row, ir.ch);
             auto get = [&](int tensor, int k, int m, const S* p) {
-                copy_async<N>((uint32_t)__cvta_generic_to_shared(slot(tensor, k, m)), p);
+                copy_async<N>(slot(tensor, k, m), p);
             };
 #pragma unroll
             for (int k = 0; k < K; ++k)
@@ -803,7 +786,7 @@ struct RowRing {
         for (int k = 0; k < K; ++k) {
             const int u = threadIdx.x + k * blockDim.x;
             if (u < U)
-                copy_async<16>((uint32_t)__cvta_generic_to_shared(slot(s, j, k)), p + u * V);
+                copy_async<16>(slot(s, j, k), p + u * V);
         }
     }
     __device__ __forceinline__ Pack<S, V> get(int s, int j, int k) const {

@@ -110,6 +110,24 @@ __device__ __forceinline__ void stream_pack(S* p, const Pack<S, V>& x) {
         store_pack(p, x);
 }
 
+// Asynchronous copies to shared memory of 4, 8 or 16 bytes.
+template <int N>
+__device__ __forceinline__ void copy_async(void* shared, const void* src) {
+    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(shared);
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N)
+                     : "memory");
+}
+__device__ __forceinline__ void copies_end_group() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Two values that go through the arithmetic together: one packed instruction
 // for each pair of fp32 operations.
 template <typename C>

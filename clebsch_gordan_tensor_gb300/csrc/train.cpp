@@ -384,10 +384,10 @@ cgtp_status cgtp_adamw_step(cgtp_dtype param_dtype, cgtp_dtype grad_dtype, int s
     if (copy && copy_dtype != CGTP_BF16 && copy_dtype != CGTP_F16)
         return tfail(CGTP_E_ARG, "copies are bfloat16 or binary16");
     if (n < 0 || (n > 0 && !tensors) || !args) return tfail(CGTP_E_ARG, "NULL argument");
-    if (!(args->eps > 0) || !(args->beta1 >= 0 && args->beta1 < 1) ||
+    if (!(args->eps >= (param_dtype == CGTP_F64 ? 0x1p-1022 : 0x1p-126)) || !(args->beta1 >= 0 && args->beta1 < 1) ||
         !(args->beta2 >= 0 && args->beta2 < 1) || args->step < 1 || !std::isfinite(args->lr) ||
         !std::isfinite(args->weight_decay))
-        return tfail(CGTP_E_ARG, "need eps > 0, 0 <= beta < 1, step >= 1, finite lr and "
+        return tfail(CGTP_E_ARG, "need a normal eps > 0, 0 <= beta < 1, step >= 1, finite lr and "
                                  "weight_decay");
     bool any = false;
     for (int i = 0; i < n; ++i) {

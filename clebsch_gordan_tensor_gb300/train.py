@@ -109,10 +109,10 @@ def embed_backward(index, grad_out, n_rows: int, scale: float = 1.0, out=None, w
     if workspace is None:
         nb = ctypes.c_size_t()
         _check(lib().cgtp_embed_backward_workspace(ty, n, n_rows, d, ctypes.byref(nb)))
-        workspace = _scratch(nb.value, grad_out.device)
+        workspace = _scratch(nb.value, grad_out.device) if nb.value else None
+    nws = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().cgtp_embed_backward(ty, bits, n, n_rows, d, index.data_ptr(), g.data, g.stride,
-                                     float(scale), out.data_ptr(), workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), _on()))
+                                     float(scale), out.data_ptr(), _at(workspace), nws, _on()))
     return out
 
 

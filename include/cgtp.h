@@ -668,7 +668,8 @@ cgtp_status cgtp_adamw_layout(int n, const int64_t* numel, int64_t* first, int64
  * copy (may be NULL): [total] in copy_dtype (CGTP_BF16 or CGTP_F16), the
  * parameters rounded to nearest in the flat layout, as plans with 16-bit
  * weights read them; not for CGTP_F64.  Tensors may have any element-aligned
- * address; flat arrays are 256-byte aligned.  eps > 0, 0 <= beta < 1, step >= 1.
+ * address; flat arrays are 256-byte aligned.  eps a normal number above 0 (in
+ * fp32, or fp64 for CGTP_F64), 0 <= beta < 1, step >= 1.
  * One launch per 64 tensors.  The scalars are passed by value: a captured graph
  * repeats the step number it was captured with. */
 cgtp_status cgtp_adamw_step(cgtp_dtype param_dtype, cgtp_dtype grad_dtype, int state_bits, int n,

@@ -31,6 +31,8 @@ EMBED = [  # n, v, d, pad, shift
     (29, 119, 32, 480, 0), (1, 1, 1, 0, 0), (1, 5, 64, 0, 0), (0, 7, 8, 0, 0), (300, 10, 33, 0, 0),
     (1000, 3, 64, 0, 0), (5000, 119, 16, 3, 0), (513, 700, 130, 0, 1), (2049, 70000, 24, 0, 0),
     (4096, 2, 256, 0, 0), (70, 4, 1000, 8, 0), (64, 1000, 2056, 0, 0), (6000, 300, 40, 0, 0),
+    (1024, 119, 64, 0, 0), (1025, 119, 64, 0, 0), (1000, 40000, 100, 4, 0), (3, 60000, 260, 0, 0),
+    (7, 256, 8, 0, 0), (2000, 255, 8, 0, 0), (2000, 65535, 8, 0, 0), (2000, 65536, 4, 0, 0),
 ]
 
 
@@ -517,7 +519,8 @@ def test_binding_refusals():
         lambda: cg.embed_forward(idx, t, out=torch.zeros(8, 4, device="cuda").t()),
         lambda: cg.embed_backward(idx, t, 5), lambda: cg.embed_backward(idx.cpu(), t[:4], 5),
         lambda: cg.embed_backward(idx, t[:4], 5, out=torch.zeros(5, 7, device="cuda")),
-        lambda: cg.embed_backward(idx, t[:4], 5, workspace=torch.zeros(16, device="cuda")),
+        lambda: cg.embed_backward(idx.repeat(800), t[:1].expand(3200, 8), 5,
+                                  workspace=torch.zeros(16, device="cuda")),
     ]
     norm = cg.IrrepsNorm("8x0e")
     w = torch.ones(8, device="cuda")
