@@ -141,7 +141,8 @@ struct NormTable {
     int n = 0, ctas = 0;
 };
 struct NormForward {
-    static constexpr int kThreads = 256, kInputs = 3;  // of a CTA; tensors read
+    static constexpr int kThreads = 256;  // of a CTA
+    int tensors() const { return 3; }     // read a row
     static constexpr int kCtas = kNormForwardCtas, kRowCtas = 152 * 4;
     int64_t n;
     double eps;
@@ -149,7 +150,8 @@ struct NormForward {
     const void *weight, *scale, *next_weight;
 };
 struct NormBackward {
-    static constexpr int kThreads = 128, kInputs = 5;
+    static constexpr int kThreads = 128;
+    int tensors() const { return grad_y.data ? 5 : 3; }
     static constexpr int kCtas = kNormBackwardCtas, kRowCtas = 152 * 2;
     int64_t n;
     double eps;

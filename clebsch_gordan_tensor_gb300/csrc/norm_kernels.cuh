@@ -176,10 +176,11 @@ __device__ __forceinline__ void forward_body(const NormIrrep& ir, int cta, const
         C s[1] = {0};
 #pragma unroll
         for (int k = 0; k < K; ++k)
+            if (K == 1 || k * T < U)
 #pragma unroll
-            for (int m = 0; m < M; ++m)
+                for (int m = 0; m < M; ++m)
 #pragma unroll
-                for (int i = 0; i < V; ++i) s[0] += q.b[k][m].get(i) * q.b[k][m].get(i);
+                    for (int i = 0; i < V; ++i) s[0] += q.b[k][m].get(i) * q.b[k][m].get(i);
         sum(s);
         const C r = rsqrt_of(s[0] * inv_d + eps);
         s[0] = 0;
@@ -517,7 +518,8 @@ __device__ __forceinline__ void backward_body(const NormIrrep& ir, int cta, cons
         }
         C s[3] = {0, 0, 0};  // b^2, h^2, next_weight gy h
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int k = 0; k < K; ++k) {
+            if (K > 1 && k * T >= U) continue;
 #pragma unroll
             for (int m = 0; m < M; ++m)
 #pragma unroll
@@ -527,12 +529,14 @@ __device__ __forceinline__ void backward_body(const NormIrrep& ir, int cta, cons
                     s[1] += x * x;
                     s[2] += x * (w2[k][i] * q.gy[k][m].get(i));
                 }
+        }
         sum(s);
         const C r = rsqrt_of(s[0] * inv_d + eps), r2 = rsqrt_of(s[1] * inv_d + eps);
         const C mean2 = s[2] * inv_d * r2 * r2;  // times h: the mean's part of gx / r'
         C gx[K][M][V], sig[K][V], P[K][V], dot[1] = {0};
 #pragma unroll
         for (int k = 0; k < K; ++k) {
+            if (K > 1 && k * T >= U) continue;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 sig[k][i] = sigmoid_of(q.z[k].get(i));
@@ -748,17 +752,31 @@ norm_backward_kernel(const __grid_constant__ NormTable tab,
 #undef CALL
 }
 
-// ---------------------------------------------------- long plain rows --
+// ------------------------------------------------------- plain rows --
 
-// Rows of scalars of more than 1 KB or so (the norm of a plain residual
-// network): the CTA takes a row at a time, a thread K vectors of it.  With so
-// few elements a thread, what counts besides the bytes are the instructions a
-// row costs whatever its length: addresses, reductions, barriers.  The row
-// number is the same for the whole CTA, so its addresses are computed once a
-// warp, and the next rows arrive in shared memory by asynchronous copies, each
-// thread copying the vectors that it reads itself: no registers for rows in
-// flight and no barrier or wait on another thread.
+// Rows of scalars only (the norm of a plain residual network) that 16-byte
+// accesses fit.  A thread takes K vectors of a row: with few elements a thread,
+// what counts besides the bytes are the instructions a row costs whatever its
+// length (addresses, reductions, barriers), so K is as large as the registers
+// allow.  Short rows go to groups of at most a warp (WARP), with no barrier; long
+// ones to a CTA, where the row number is the same for all threads and its
+// addresses are computed once a warp.  The next rows arrive in shared memory by
+// asynchronous copies, each thread copying the vectors that it reads itself: no
+// registers for rows in flight and no wait on another thread.  Arithmetic in
+// pairs.
 constexpr int kStages = 2;
+constexpr int kRowThreads = 256;
+
+// Where a thread stands: thread t of T in its group, which takes every G-th row.
+template <bool WARP>
+struct RowPlace {
+    int T, t, group, G;
+    __device__ __forceinline__ explicit RowPlace(const NormIrrep& ir)
+        : T(WARP ? ir.T : blockDim.x),
+          t(WARP ? threadIdx.x & (ir.T - 1) : threadIdx.x),
+          group(WARP ? threadIdx.x / ir.T : 0),
+          G(WARP ? kRowThreads / ir.T : 1) {}
+};
 
 // A thread's vectors of N tensors in kStages stages; tensor j's vector k of
 // stage s at ((s N + j) K + k) threads + thread, 16 bytes each.
@@ -766,31 +784,28 @@ template <typename S, int N, int K>
 struct RowRing {
     static constexpr int V = 16 / sizeof(S);
     unsigned char* mine;
-    int U;
-    __device__ __forceinline__ unsigned char* slot(int s, int j, int k) const {
-        return mine + (size_t)((s * N + j) * K + k) * blockDim.x * 16;
+    int T, t, U;
+    __device__ __forceinline__ Pack<S, V>* slot(int s, int j, int k) const {
+        return reinterpret_cast<Pack<S, V>*>(mine +
+                                             (size_t)((s * N + j) * K + k) * blockDim.x * 16);
     }
-    // Absent tensors and the threads past the row's end keep these values.
-    __device__ __forceinline__ void fill(int j, typename Compute<S>::type missing) {
+    // Absent tensors, threads past the row's end and groups without a row have
+    // these values: zeros, and for the gate, the last tensor, infinity.
+    __device__ __forceinline__ void fill(int s) {
         Pack<S, V> x;
-        x.fill(missing);
 #pragma unroll
-        for (int s = 0; s < kStages; ++s)
+        for (int j = 0; j < N; ++j) {
+            x.fill(j == N - 1 ? INFINITY : 0);
 #pragma unroll
-            for (int k = 0; k < K; ++k) *reinterpret_cast<Pack<S, V>*>(slot(s, j, k)) = x;
+            for (int k = 0; k < K; ++k) *slot(s, j, k) = x;
+        }
     }
     __device__ __forceinline__ void fetch(int s, int j, const cgtp_rows& q, int64_t row, int at) {
         if (!q.data) return;
         const S* p = (const S*)q.data + row * q.stride + at;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int u = threadIdx.x + k * blockDim.x;
-            if (u < U)
-                copy_async<16>(slot(s, j, k), p + u * V);
-        }
-    }
-    __device__ __forceinline__ Pack<S, V> get(int s, int j, int k) const {
-        return *reinterpret_cast<const Pack<S, V>*>(slot(s, j, k));
+        for (int k = 0; k < K; ++k)
+            if (t + k * T < U) copy_async<16>(slot(s, j, k), p + (t + k * T) * V);
     }
 };
 
@@ -805,14 +820,14 @@ __device__ __forceinline__ void load_twos(Two<C> (&out)[H], const C* p, int at) 
         out[i] = p ? Two<C>{p[at + 2 * i], p[at + 2 * i + 1]} : Two<C>{(C)1, (C)1};
 }
 
-// Sums over a CTA of up to eight warps for the row kernels: R values, 1 or 3.
-// A warp's lanes share the work of three values (6 shuffles, not 15), and after
-// the barrier every thread adds the warps' sums from vector loads, so that no
-// further shuffle is on the path.  Two sets of slots in turn, as GroupSum.
-template <typename C>
+// Sums of R values over a group.  Over a CTA of up to eight warps a warp's lanes
+// share the work of three values (6 shuffles, not 15), and after the barrier
+// every thread adds the warps' sums from vector loads, so that no further
+// shuffle is on the path; two sets of slots in turn, as GroupSum.
+template <typename C, bool WARP>
 struct RowSum {
     C (*buf)[8];  // [2][3][8], zero past the CTA's warps
-    int flip = 0;
+    int T, flip = 0;
     __device__ __forceinline__ C* side() {
         C* p = &buf[3 * flip][0];
         flip ^= 1;
@@ -824,52 +839,64 @@ struct RowSum {
         for (int i = 0; i < 8; ++i) x[i] = p[i];
         return ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
     }
-    __device__ __forceinline__ void operator()(C (&v)[1]) {
-        C* p = side();
+    template <int R>
+    __device__ __forceinline__ void operator()(C (&v)[R]) {
+        if constexpr (WARP) {
+            for (int o = T >> 1; o > 0; o >>= 1)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
-        if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = v[0];
-        __syncthreads();
-        v[0] = total(p);
-    }
-    __device__ __forceinline__ void operator()(C (&v)[3]) {
-        C* p = side();
-        const int lane = threadIdx.x & 31;
-        // the lower half keeps values 0 and 1, the upper half 2 and a zero
-        const bool up = lane & 16;
-        C x = up ? v[2] : v[0], y = up ? (C)0 : v[1];
-        x += __shfl_xor_sync(0xFFFFFFFFu, up ? v[0] : v[2], 16);
-        y += __shfl_xor_sync(0xFFFFFFFFu, up ? v[1] : (C)0, 16);
-        const bool odd = lane & 8;  // then one value a lane: 0, 1, 2 or none
-        C z = (odd ? y : x) + __shfl_xor_sync(0xFFFFFFFFu, odd ? x : y, 8);
+                for (int r = 0; r < R; ++r) v[r] += __shfl_xor_sync(0xFFFFFFFFu, v[r], o);
+        } else if constexpr (R == 1) {
+            C* p = side();
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
-        if ((lane & 7) == 0 && lane < 24) p[(lane >> 3) * 8 + (threadIdx.x >> 5)] = z;
-        __syncthreads();
+            for (int o = 16; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+            if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = v[0];
+            __syncthreads();
+            v[0] = total(p);
+        } else {
+            static_assert(R == 3);
+            C* p = side();
+            const int lane = threadIdx.x & 31;
+            // the lower half keeps values 0 and 1, the upper half 2 and a zero
+            const bool up = lane & 16;
+            C x = up ? v[2] : v[0], y = up ? (C)0 : v[1];
+            x += __shfl_xor_sync(0xFFFFFFFFu, up ? v[0] : v[2], 16);
+            y += __shfl_xor_sync(0xFFFFFFFFu, up ? v[1] : (C)0, 16);
+            const bool odd = lane & 8;  // then one value a lane: 0, 1, 2 or none
+            C z = (odd ? y : x) + __shfl_xor_sync(0xFFFFFFFFu, odd ? x : y, 8);
 #pragma unroll
-        for (int r = 0; r < 3; ++r) v[r] = total(p + 8 * r);
+            for (int o = 4; o > 0; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+            if ((lane & 7) == 0 && lane < 24) p[(lane >> 3) * 8 + (threadIdx.x >> 5)] = z;
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < 3; ++r) v[r] = total(p + 8 * r);
+        }
     }
 };
 
-template <typename S, int K>
-__global__ void __launch_bounds__(256, 2)
+template <typename C>
+__device__ __forceinline__ void clear(C (&sums)[6][8]) {
+    for (int i = threadIdx.x; i < 48; i += blockDim.x) (&sums[0][0])[i] = 0;
+    __syncthreads();
+}
+
+template <typename S, int K, bool WARP>
+__global__ void __launch_bounds__(kRowThreads, 2)
 row_forward_kernel(const __grid_constant__ NormTable tab, const __grid_constant__ NormForward a) {
     using C = typename Compute<S>::type;
     constexpr int V = 16 / sizeof(S), H = V / 2;
     __shared__ __align__(16) C sums[6][8];
-    if (threadIdx.x < 48) (&sums[0][0])[threadIdx.x] = 0;
-    if (blockDim.x < 64 && threadIdx.x < 16) (&sums[4][0])[threadIdx.x] = 0;
-    __syncthreads();
     extern __shared__ __align__(16) unsigned char dynamic[];
+    clear(sums);
     int i = 0;
     while (i + 1 < tab.n && (int)blockIdx.x >= tab.ir[i + 1].cta0) ++i;
     const NormIrrep& ir = tab.ir[i];
-    const int B = blockDim.x, t = threadIdx.x, U = ir.mul / V;
+    const RowPlace<WARP> w(ir);
+    const int U = ir.mul / V, T = w.T, t = w.t;
     const C inv_d = (C)1 / (C)ir.mul, eps = (C)a.eps;
     Two<C> coef[K][H], next[K][H];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int c = ir.ch + (t + k * B < U ? t + k * B : 0) * V;
+        const int c = ir.ch + (t + k * T < U ? t + k * T : 0) * V;
         Two<C> sc[H];
         load_twos(coef[k], (const C*)a.weight, c);
         load_twos(sc, (const C*)a.scale, c);
@@ -877,10 +904,7 @@ row_forward_kernel(const __grid_constant__ NormTable tab, const __grid_constant_
 #pragma unroll
         for (int j = 0; j < H; ++j) coef[k][j] = coef[k][j] * sc[j];
     }
-    RowRing<S, 3, K> ring{dynamic + t * 16, U};
-    ring.fill(0, 0);
-    ring.fill(1, 0);
-    ring.fill(2, INFINITY);
+    RowRing<S, 3, K> ring{dynamic + threadIdx.x * 16, T, t, U};
     auto fetch = [&](int st, int64_t row) {
         if (row < a.n) {
             ring.fetch(st, 0, a.b, row, ir.off);
@@ -889,16 +913,22 @@ row_forward_kernel(const __grid_constant__ NormTable tab, const __grid_constant_
         }
         copies_end_group();
     };
-    RowSum<C> sum{sums};
-    int64_t row = blockIdx.x - ir.cta0;
-    for (int st = 0; st < kStages; ++st) fetch(st, row + (int64_t)st * ir.ctas);
-    for (int st = 0; row < a.n; row += ir.ctas, st = st + 1 == kStages ? 0 : st + 1) {
+    RowSum<C, WARP> sum{sums, T};
+    const int64_t step = (int64_t)ir.ctas * w.G;
+    int64_t base = (int64_t)(blockIdx.x - ir.cta0) * w.G;
+    for (int st = 0; st < kStages; ++st) {
+        ring.fill(st);
+        fetch(st, base + w.group + st * step);
+    }
+    for (int st = 0; base < a.n; base += step, st = st + 1 == kStages ? 0 : st + 1) {
+        const int64_t row = base + w.group;
+        const bool in = !WARP || row < a.n;
         copies_wait<kStages - 1>();
         Pack<S, V> b[K];
         Two<C> part{0, 0};
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            b[k] = ring.get(st, 0, k);
+            b[k] = *ring.slot(st, 0, k);
 #pragma unroll
             for (int j = 0; j < H; ++j) part = fma(two_at(b[k], j), two_at(b[k], j), part);
         }
@@ -910,8 +940,7 @@ row_forward_kernel(const __grid_constant__ NormTable tab, const __grid_constant_
         S* h = (S*)a.h.data + row * a.h.stride + ir.off;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const Pack<S, V> x = ring.get(st, 1, k);
-            const Pack<S, V> z = ring.get(st, 2, k);
+            const Pack<S, V> x = *ring.slot(st, 1, k), z = *ring.slot(st, 2, k);
             Two<C> v[H];
 #pragma unroll
             for (int j = 0; j < H; ++j)
@@ -920,9 +949,9 @@ row_forward_kernel(const __grid_constant__ NormTable tab, const __grid_constant_
             set_twos(b[k], v);
 #pragma unroll
             for (int j = 0; j < H; ++j) part = fma(two_at(b[k], j), two_at(b[k], j), part);
-            if (t + k * B < U) store_pack(h + (t + k * B) * V, b[k]);
+            if (in && t + k * T < U) store_pack(h + (t + k * T) * V, b[k]);
         }
-        fetch(st, row + (int64_t)kStages * ir.ctas);
+        fetch(st, row + kStages * step);
         if (a.y.data) {
             s[0] = part.x + part.y;
             sum(s);
@@ -935,96 +964,116 @@ row_forward_kernel(const __grid_constant__ NormTable tab, const __grid_constant_
                 for (int j = 0; j < H; ++j)
                     v[j] = two_at(b[k], j) * (Two<C>{r2, r2} * next[k][j]);
                 set_twos(b[k], v);
-                if (t + k * B < U) store_pack(y + (t + k * B) * V, b[k]);
+                if (in && t + k * T < U) store_pack(y + (t + k * T) * V, b[k]);
             }
         }
     }
     copies_wait<0>();
 }
 
-template <typename S, int K>
-__global__ void __launch_bounds__(256, K * 16 / sizeof(S) > 16 ? 1 : 2)
+// NEXT: with the gradient through the next norm.
+template <typename S, int K, bool WARP, bool NEXT>
+__global__ void __launch_bounds__(kRowThreads, K * 16 / sizeof(S) > 16 && NEXT ? 1 : 2)
 row_backward_kernel(const __grid_constant__ NormTable tab, const __grid_constant__ NormBackward a) {
     using C = typename Compute<S>::type;
-    constexpr int V = 16 / sizeof(S), H = V / 2;
+    constexpr int V = 16 / sizeof(S), H = V / 2, N = NEXT ? 5 : 3, KN = NEXT ? K : 1;
     __shared__ __align__(16) C sums[6][8];
-    if (threadIdx.x < 48) (&sums[0][0])[threadIdx.x] = 0;
-    if (blockDim.x < 64 && threadIdx.x < 16) (&sums[4][0])[threadIdx.x] = 0;
-    __syncthreads();
     extern __shared__ __align__(16) unsigned char dynamic[];
+    clear(sums);
     int i = 0;
     while (i + 1 < tab.n && (int)blockIdx.x >= tab.ir[i + 1].cta0) ++i;
     const NormIrrep& ir = tab.ir[i];
-    const int cta = blockIdx.x - ir.cta0, B = blockDim.x, t = threadIdx.x, U = ir.mul / V;
+    const RowPlace<WARP> w(ir);
+    const int cta = blockIdx.x - ir.cta0, U = ir.mul / V, T = w.T, t = w.t;
     const C inv_d = (C)1 / (C)ir.mul, eps = (C)a.eps;
-    Two<C> ws[K][H], w2[K][H], acc_a[K][H], acc_q[K][H];
+    Two<C> ws[K][H], acc_a[K][H], w2[KN][H], acc_q[KN][H];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int c = ir.ch + (t + k * B < U ? t + k * B : 0) * V;
+        const int c = ir.ch + (t + k * T < U ? t + k * T : 0) * V;
         Two<C> sc[H];
         load_twos(ws[k], (const C*)a.weight, c);
         load_twos(sc, (const C*)a.scale, c);
-        load_twos(w2[k], (const C*)a.next_weight, c);
+        if constexpr (NEXT) load_twos(w2[k], (const C*)a.next_weight, c);
 #pragma unroll
         for (int j = 0; j < H; ++j) {
             ws[k][j] = ws[k][j] * sc[j];
-            acc_a[k][j] = acc_q[k][j] = {0, 0};
+            acc_a[k][j] = {0, 0};
+            if constexpr (NEXT) acc_q[k][j] = {0, 0};
         }
     }
-    RowRing<S, 5, K> ring{dynamic + t * 16, U};
-    for (int j = 0; j < 4; ++j) ring.fill(j, 0);
-    ring.fill(4, INFINITY);
+    RowRing<S, N, K> ring{dynamic + threadIdx.x * 16, T, t, U};
     auto fetch = [&](int st, int64_t row) {
         if (row < a.n) {
             ring.fetch(st, 0, a.b, row, ir.off);
-            if (a.grad_y.data) ring.fetch(st, 1, a.h, row, ir.off);
-            ring.fetch(st, 2, a.grad_y, row, ir.off);
-            ring.fetch(st, 3, a.grad_h, row, ir.off);
-            ring.fetch(st, 4, a.gate, row, ir.ch);
+            ring.fetch(st, 1, a.grad_h, row, ir.off);
+            if constexpr (NEXT) {
+                ring.fetch(st, 2, a.h, row, ir.off);
+                ring.fetch(st, 3, a.grad_y, row, ir.off);
+            }
+            ring.fetch(st, N - 1, a.gate, row, ir.ch);
         }
         copies_end_group();
     };
-    RowSum<C> sum{sums};
-    int64_t row = cta;
-    for (int st = 0; st < kStages; ++st) fetch(st, row + (int64_t)st * ir.ctas);
-    for (int st = 0; row < a.n; row += ir.ctas, st = st + 1 == kStages ? 0 : st + 1) {
+    RowSum<C, WARP> sum{sums, T};
+    const int64_t step = (int64_t)ir.ctas * w.G;
+    int64_t base = (int64_t)cta * w.G;
+    for (int st = 0; st < kStages; ++st) {
+        ring.fill(st);
+        fetch(st, base + w.group + st * step);
+    }
+    for (int st = 0; base < a.n; base += step, st = st + 1 == kStages ? 0 : st + 1) {
+        const int64_t row = base + w.group;
+        const bool in = !WARP || row < a.n;
         copies_wait<kStages - 1>();
-        Pack<S, V> b[K], h[K], y[K];
+        if (!in) ring.fill(st);  // adds nothing to the channel sums
+        Pack<S, V> b[K], h[KN], y[KN];
+        C r, r2 = 0, mean2 = 0;
         Two<C> p0{0, 0}, p1{0, 0}, p2{0, 0};  // b^2, h^2, next_weight gy h
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            b[k] = ring.get(st, 0, k);
-            h[k] = ring.get(st, 1, k);
-            y[k] = ring.get(st, 2, k);
+            b[k] = *ring.slot(st, 0, k);
 #pragma unroll
-            for (int j = 0; j < H; ++j) {
-                const Two<C> v = two_at(b[k], j), x = two_at(h[k], j);
-                p0 = fma(v, v, p0);
-                p1 = fma(x, x, p1);
-                p2 = fma(x, w2[k][j] * two_at(y[k], j), p2);
+            for (int j = 0; j < H; ++j) p0 = fma(two_at(b[k], j), two_at(b[k], j), p0);
+            if constexpr (NEXT) {
+                h[k] = *ring.slot(st, 2, k);
+                y[k] = *ring.slot(st, 3, k);
+#pragma unroll
+                for (int j = 0; j < H; ++j) {
+                    const Two<C> x = two_at(h[k], j);
+                    p1 = fma(x, x, p1);
+                    p2 = fma(x, w2[k][j] * two_at(y[k], j), p2);
+                }
             }
         }
-        C s[3] = {p0.x + p0.y, p1.x + p1.y, p2.x + p2.y};
-        sum(s);
-        const C r = rsqrt_of(s[0] * inv_d + eps), r2 = rsqrt_of(s[1] * inv_d + eps);
-        const C mean2 = -s[2] * inv_d * r2 * r2;
+        if constexpr (NEXT) {
+            C s[3] = {p0.x + p0.y, p1.x + p1.y, p2.x + p2.y};
+            sum(s);
+            r = rsqrt_of(s[0] * inv_d + eps);
+            r2 = rsqrt_of(s[1] * inv_d + eps);
+            mean2 = -s[2] * inv_d * r2 * r2;
+        } else {
+            C s[1] = {p0.x + p0.y};
+            sum(s);
+            r = rsqrt_of(s[0] * inv_d + eps);
+        }
         const Two<C> rr{r, r}, rr2{r2, r2}, mm2{mean2, mean2};
         Two<C> gx[K][H], dot{0, 0};
         S* oz = a.grad_gate.data ? (S*)a.grad_gate.data + row * a.grad_gate.stride + ir.ch : nullptr;
         S* ox = a.grad_x.data ? (S*)a.grad_x.data + row * a.grad_x.stride + ir.off : nullptr;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const Pack<S, V> gh = ring.get(st, 3, k);
-            const Pack<S, V> z = ring.get(st, 4, k);
+            const Pack<S, V> gh = *ring.slot(st, 1, k), z = *ring.slot(st, N - 1, k);
             Two<C> f[H], v[H];
             Pack<S, V> p;
 #pragma unroll
             for (int j = 0; j < H; ++j) {
-                const Two<C> x = two_at(h[k], j), gy = two_at(y[k], j);
-                const Two<C> sig = sigmoid_of(two_at(z, j));
-                gx[k][j] = fma(rr2, fma(x, mm2, w2[k][j] * gy), two_at(gh, j));
-                acc_q[k][j] = fma(gy, x * rr2, acc_q[k][j]);
-                const Two<C> rs = rr * sig;
+                gx[k][j] = two_at(gh, j);
+                if constexpr (NEXT) {
+                    const Two<C> x = two_at(h[k], j), gy = two_at(y[k], j);
+                    gx[k][j] = fma(rr2, fma(x, mm2, w2[k][j] * gy), gx[k][j]);
+                    acc_q[k][j] = fma(gy, x * rr2, acc_q[k][j]);
+                }
+                const Two<C> sig = sigmoid_of(two_at(z, j)), rs = rr * sig;
                 const Two<C> P = gx[k][j] * two_at(b[k], j) * rs;
                 acc_a[k][j] = acc_a[k][j] + P;
                 const Two<C> wp = ws[k][j] * P;
@@ -1032,15 +1081,19 @@ row_backward_kernel(const __grid_constant__ NormTable tab, const __grid_constant
                 v[j] = wp * fma(sig, Two<C>{-1, -1}, Two<C>{1, 1});
                 f[j] = ws[k][j] * rs;
             }
-            const bool on = t + k * B < U;
-            set_twos(p, v);
-            if (oz && on) store_pack(oz + (t + k * B) * V, p);
-            set_twos(p, gx[k]);
-            if (ox && on) store_pack(ox + (t + k * B) * V, p);
+            const bool on = in && t + k * T < U;
+            if (oz) {
+                set_twos(p, v);
+                if (on) store_pack(oz + (t + k * T) * V, p);
+            }
+            if (ox) {
+                set_twos(p, gx[k]);
+                if (on) store_pack(ox + (t + k * T) * V, p);
+            }
 #pragma unroll
             for (int j = 0; j < H; ++j) gx[k][j] = gx[k][j] * f[j];
         }
-        fetch(st, row + (int64_t)kStages * ir.ctas);
+        fetch(st, row + kStages * step);
         C d[1] = {dot.x + dot.y};
         sum(d);
         const C mean = -d[0] * inv_d * r * r;
@@ -1053,22 +1106,38 @@ row_backward_kernel(const __grid_constant__ NormTable tab, const __grid_constant
                 for (int j = 0; j < H; ++j)
                     v[j] = fma(two_at(b[k], j), Two<C>{mean, mean}, gx[k][j]);
                 set_twos(b[k], v);
-                if (t + k * B < U) store_pack(ob + (t + k * B) * V, b[k]);
+                if (in && t + k * T < U) store_pack(ob + (t + k * T) * V, b[k]);
             }
         }
     }
     copies_wait<0>();
     if (!a.partial) return;
     C* out = partial_row<C>(ir, cta, a);
+    // The groups' sums, added in group order through shared memory.
+    C* rows = reinterpret_cast<C*>(dynamic);
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-        if (t + k * B < U)
+    for (int which = 0; which < 2; ++which) {
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int j = 0; j < H; ++j) {
-                C* o = out + (t + k * B) * V + 2 * j;
-                o[0] = acc_a[k][j].x, o[1] = acc_a[k][j].y;
-                o[ir.mul] = acc_q[k][j].x, o[ir.mul + 1] = acc_q[k][j].y;
+                Two<C> x = acc_a[k][j];
+                if (which == 1) {
+                    x = {0, 0};
+                    if constexpr (NEXT) x = acc_q[k][j];
+                }
+                C* o = rows + (threadIdx.x * K + k) * V + 2 * j;
+                o[0] = x.x, o[1] = x.y;
             }
+        __syncthreads();
+        for (int c = threadIdx.x; c < ir.mul; c += blockDim.x) {
+            const int u = c / V, k = u / T;
+            C s = 0;
+            for (int g = 0; g < w.G; ++g) s += rows[((g * T + u % T) * K + k) * V + c % V];
+            out[which * ir.mul + c] = s;
+        }
+    }
 }
 
 // Adds the CTAs' partial rows: 32 sums a CTA, a warp for every 32nd row, joined
@@ -1112,8 +1181,9 @@ template <int V>
 int shape_table(NormTable& tab, int64_t n, int threads, int& most_k, int& most_l) {
     most_l = 0;
     for (int i = 0; i < tab.n; ++i) most_l = std::max(most_l, tab.ir[i].l);
-    const int most_t = most_l == 0 ? 512 : threads;
-    if (most_l == 0) threads = 256;
+    const bool plain = most_l == 0 && V != 8;
+    const int most_t = plain ? 512 : threads;
+    if (plain) threads = 256;
     const int least = V > 1 ? 1 : 4, most = V == 1 ? 16 : V == 8 ? 2 : 4;
     most_k = least;
     for (int i = 0; i < tab.n; ++i) {
@@ -1198,21 +1268,23 @@ cudaError_t launch(const NormTable& tab, int threads, const NormBackward& a, cud
     return e != cudaSuccess ? e : finish<C>(tab, a, s);
 }
 
-template <typename S, int K>
+template <typename S, int K, bool WARP>
 const void* row_kernel(const NormForward&) {
-    return (const void*)row_forward_kernel<S, K>;
+    return (const void*)row_forward_kernel<S, K, WARP>;
 }
-template <typename S, int K>
-const void* row_kernel(const NormBackward&) {
-    return (const void*)row_backward_kernel<S, K>;
+template <typename S, int K, bool WARP>
+const void* row_kernel(const NormBackward& a) {
+    return a.grad_y.data ? (const void*)row_backward_kernel<S, K, WARP, true>
+                         : (const void*)row_backward_kernel<S, K, WARP, false>;
 }
-template <typename S, int K, typename Args>
+
+template <typename S, int K, bool WARP, typename Args>
 cudaError_t launch_rows(const NormTable& tab, int threads, const Args& a, cudaStream_t s) {
-    const void* f = row_kernel<S, K>(a);
-    const size_t smem = (size_t)kStages * Args::kInputs * K * threads * 16;
-    static std::atomic<uint32_t> done{0};
-    cudaError_t e = allow_smem(f, done);
+    const void* f = row_kernel<S, K, WARP>(a);
+    static std::atomic<uint32_t> done[2];
+    cudaError_t e = allow_smem(f, done[a.tensors() > 3]);
     if (e != cudaSuccess) return e;
+    const size_t smem = (size_t)kStages * a.tensors() * K * threads * 16;
     void* args[] = {const_cast<NormTable*>(&tab), const_cast<Args*>(&a)};
     e = cudaLaunchKernel(f, dim3(tab.ctas), dim3(threads), args, smem, s);
     count_launch();
@@ -1220,50 +1292,71 @@ cudaError_t launch_rows(const NormTable& tab, int threads, const Args& a, cudaSt
     return finish<typename Compute<S>::type>(tab, a, s);
 }
 
-// Rows of scalars only, of 64 to 1024 vectors of 16 bytes.
+// Rows of scalars only, of up to 1024 vectors of 16 bytes: two a thread, in the
+// longest rows four; a warp takes up to 64 of them.  (Four a thread and a warp
+// for 128: 55 us, a CTA of 64 threads with two each: 51 us for the norm of 65,536
+// rows of 1024 bf16.)
 template <typename S, typename Args>
-bool rows_apply(NormTable& tab, int64_t n, int& threads, int& K) {
+bool rows_apply(NormTable& tab, const Args& a, int& threads, int& K, bool& warp) {
     constexpr int V = 16 / sizeof(S);
     int most = 0;
     for (int i = 0; i < tab.n; ++i) {
         if (tab.ir[i].l != 0) return false;
         most = std::max(most, tab.ir[i].mul / V);
     }
-    if (most < 64 || most > 1024) return false;
+    if (most > 1024) return false;
     K = most > 512 ? 4 : 2;
-    threads = 32;
+    warp = most <= 64;
+    threads = warp ? kRowThreads : 64;
     while (threads * K < most) threads *= 2;
     tab.ctas = 0;
     for (int i = 0; i < tab.n; ++i) {
         NormIrrep& ir = tab.ir[i];
         ir.K = K;
-        ir.T = threads;
+        ir.T = warp ? 1 : threads;
+        while (ir.T * K < ir.mul / V) ir.T *= 2;
+        const int64_t G = threads / ir.T;
+        // the shares of row kernels' CTAs, which take more of an SM
         const int most_ctas = std::min(
-            ir.max_ctas, std::max(1, ir.max_ctas * Args::kRowCtas / Args::kCtas * 256 / threads));
-        ir.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(most_ctas, n));
+            ir.max_ctas,
+            std::max(1, ir.max_ctas * Args::kRowCtas / Args::kCtas * kRowThreads / threads));
+        ir.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(most_ctas, (a.n + G - 1) / G));
         ir.cta0 = tab.ctas;
         tab.ctas += ir.ctas;
     }
     return true;
 }
 
+template <typename S, typename Args>
+cudaError_t launch_rows(const NormTable& tab, int threads, int K, bool warp, const Args& a,
+                        cudaStream_t s) {
+    if (K == 4) return launch_rows<S, 4, false>(tab, threads, a, s);
+    return warp ? launch_rows<S, 2, true>(tab, threads, a, s)
+                : launch_rows<S, 2, false>(tab, threads, a, s);
+}
+
 template <typename S, int V, typename Args>
 cudaError_t launch_v(NormTable tab, const Args& a, cudaStream_t s) {
     int k, l;
-    if constexpr (V * sizeof(S) == 16) {
+    constexpr bool rows = V * sizeof(S) == 16;
+    if constexpr (rows) {
         int threads;
-        if (rows_apply<S, Args>(tab, a.n, threads, k))
-            return k == 2 ? launch_rows<S, 2>(tab, threads, a, s)
-                          : launch_rows<S, 4>(tab, threads, a, s);
+        bool warp;
+        if (rows_apply<S>(tab, a, threads, k, warp)) return launch_rows<S>(tab, threads, k, warp, a, s);
     }
     const int threads = shape_table<V>(tab, a.n, Args::kThreads, k, l);
     constexpr int least = V > 1 ? 1 : 4;
     if (l > 3) return launch<S, V, 6, least>(tab, threads, a, s);
-    if (l > 0) return launch<S, V, 3, least>(tab, threads, a, s);
-    if (k == least) return launch<S, V, 0, least>(tab, threads, a, s);
-    if constexpr (V < 8)
-        if (k == 4 * least) return launch<S, V, 0, 4 * least>(tab, threads, a, s);
-    return launch<S, V, 0, 2 * least>(tab, threads, a, s);
+    // past the row kernels eight 16-bit channels leave the body that reads again
+    if (l > 0 || V == 8) return launch<S, V, 3, least>(tab, threads, a, s);
+    if constexpr (V < 8) {
+        if constexpr (!rows) {
+            if (k == least) return launch<S, V, 0, least>(tab, threads, a, s);
+            if (k == 2 * least) return launch<S, V, 0, 2 * least>(tab, threads, a, s);
+        }
+        return launch<S, V, 0, 4 * least>(tab, threads, a, s);
+    }
+    return cudaErrorInvalidValue;  // not reached
 }
 
 template <typename S, typename Args>
