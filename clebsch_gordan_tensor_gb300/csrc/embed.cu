@@ -94,9 +94,8 @@ embed_forward_kernel(int64_t n, int64_t v, int64_t d, int T, const I* __restrict
 
 // At most one CTA an SM, each with its own range of positions, so that every
 // CTA can add up all counts before it by itself: a pass is two launches.
-constexpr int kTile = 1024;  // positions taken at a time
-constexpr int kSortThreads = 256, kSortWarps = kSortThreads / 32;
-constexpr int kPerWarp = kTile / kSortWarps;
+constexpr int kTile = 1024;  // positions taken at a time, one a thread
+constexpr int kSortThreads = kTile, kSortWarps = kSortThreads / 32;
 constexpr int kSortCtas = 152;
 
 template <typename I>
@@ -120,113 +119,105 @@ template <typename I>
 __global__ void __launch_bounds__(kSortThreads)
 sort_count_kernel(uint32_t n, uint32_t v, uint32_t range, int shift, const I* __restrict__ in,
                   uint32_t* __restrict__ hist, uint32_t* __restrict__ marks, uint32_t mark_words) {
-    __shared__ uint32_t count[kSortWarps][256];
-    const int warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int w = 0; w < kSortWarps; ++w) count[w][threadIdx.x] = 0;
+    constexpr int kCopies = 8;  // of the counters, against warps that meet in one
+    __shared__ uint32_t count[kCopies][256];
+    for (int i = threadIdx.x; i < kCopies * 256; i += kSortThreads) (&count[0][0])[i] = 0;
     for (uint32_t i = blockIdx.x * kSortThreads + threadIdx.x; i < mark_words;
          i += gridDim.x * kSortThreads)
         marks[i] = 0;
     __syncthreads();
     const uint32_t first = blockIdx.x * range, last = min(first + range, n);
-    uint32_t i = first + threadIdx.x;
-    for (; i + 7 * kSortThreads < last; i += 8 * kSortThreads) {
-        I x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = in[i + j * kSortThreads];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            atomicAdd(&count[warp][key_of(x[j], v) >> shift & 255u], 1u);
-    }
-    for (; i < last; i += kSortThreads)
-        atomicAdd(&count[warp][key_of(in[i], v) >> shift & 255u], 1u);
+    uint32_t* mine = count[(threadIdx.x >> 5) % kCopies];
+    for (uint32_t i = first + threadIdx.x; i < last; i += kSortThreads)
+        atomicAdd(&mine[key_of(in[i], v) >> shift & 255u], 1u);
     __syncthreads();
-    uint32_t s = 0;
+    if (threadIdx.x < 256) {
+        uint32_t s = 0;
 #pragma unroll
-    for (int w = 0; w < kSortWarps; ++w) s += count[w][threadIdx.x];
-    hist[blockIdx.x * 256 + threadIdx.x] = s;
+        for (int w = 0; w < kCopies; ++w) s += count[w][threadIdx.x];
+        hist[blockIdx.x * 256 + threadIdx.x] = s;
+    }
 }
 
-// Stable: a warp owns consecutive positions of a tile and takes them 32 at a
-// time; a position's place is its digit's base plus the equal digits before it.
+// Stable: a warp owns 32 consecutive positions of a tile; a position's place is
+// its digit's base plus the equal digits before it.
 template <typename I>
 __global__ void __launch_bounds__(kSortThreads)
 sort_scatter_kernel(uint32_t n, uint32_t v, uint32_t range, int shift, const I* __restrict__ in,
                     const uint32_t* __restrict__ pos_in, const uint32_t* __restrict__ hist,
                     uint32_t* __restrict__ keys, uint32_t* __restrict__ pos) {
     __shared__ uint32_t count[kSortWarps][256];
-    __shared__ uint32_t warp_sum[kSortWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // digit threadIdx.x: its count in all CTAs and in those before this one
+    __shared__ uint32_t warp_sum[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, digit = threadIdx.x & 255;
+    // a digit's count in all CTAs and in those before this one: a quarter of the
+    // threads for every fourth CTA
     uint32_t all = 0, before = 0;
-    for (uint32_t first = 0; first < gridDim.x; first += 32) {
-        uint32_t x[32];
+    {
+        const uint32_t part = threadIdx.x >> 8;
+        for (uint32_t first = part; first < gridDim.x; first += 4 * 32) {
+            uint32_t x[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            x[j] = first + j < gridDim.x ? hist[(first + j) * 256 + threadIdx.x] : 0;
+            for (int j = 0; j < 32; ++j)
+                x[j] = first + 4 * j < gridDim.x ? hist[(first + 4 * j) * 256 + digit] : 0;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            all += x[j];
-            before += first + j < blockIdx.x ? x[j] : 0;
+            for (int j = 0; j < 32; ++j) {
+                all += x[j];
+                before += first + 4 * j < blockIdx.x ? x[j] : 0;
+            }
         }
+        count[part][digit] = all;
+        count[4 + part][digit] = before;
     }
-    uint32_t inc = all;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= o) inc += x;
-    }
-    if (lane == 31) warp_sum[warp] = inc;
     __syncthreads();
-    uint32_t base = inc - all + before;
+    uint32_t base = 0;
+    if (threadIdx.x < 256) {
+        all = count[0][digit] + count[1][digit] + count[2][digit] + count[3][digit];
+        before = count[4][digit] + count[5][digit] + count[6][digit] + count[7][digit];
+        uint32_t inc = all;
 #pragma unroll
-    for (int w = 0; w < kSortWarps; ++w) base += w < warp ? warp_sum[w] : 0;
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += x;
+        }
+        if (lane == 31) warp_sum[warp] = inc;
+        base = inc - all + before;
+    }
+    __syncthreads();
+    if (threadIdx.x < 256)
+#pragma unroll
+        for (int w = 0; w < 8; ++w) base += w < warp ? warp_sum[w] : 0;
 
     const uint32_t first = blockIdx.x * range, last = min(first + range, n);
     for (uint32_t tile = first; tile < last; tile += kTile) {
+        const uint32_t i = tile + threadIdx.x;
+        const bool on = i < last;
+        const uint32_t key = on ? key_of(in[i], v) : 0;
+        const uint32_t from = on && pos_in ? pos_in[i] : i;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kSortWarps; ++w) count[w][threadIdx.x] = 0;
+        for (int j = 0; j < 256 / 32; ++j) count[warp][j * 32 + lane] = 0;
+        __syncwarp();
+        const uint32_t dig = on ? key >> shift & 255u : 256u;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, dig);
+        const uint32_t low = same & ((1u << lane) - 1);
+        if (on && low == 0) count[warp][dig] = __popc(same);
         __syncthreads();
-        uint32_t key[kPerWarp / 32], at[kPerWarp / 32];
-        uint32_t from[kPerWarp / 32];
-#pragma unroll
-        for (int j = 0; j < kPerWarp / 32; ++j) {
-            const uint32_t i = tile + warp * kPerWarp + j * 32 + lane;
-            key[j] = i < last ? key_of(in[i], v) : 0xFFFFFFFFu;
-            from[j] = pos_in && i < last ? pos_in[i] : i;
-        }
-        // place among the warp's equal digits
-#pragma unroll
-        for (int j = 0; j < kPerWarp / 32; ++j) {
-            const bool on = key[j] != 0xFFFFFFFFu;
-            const uint32_t dig = on ? key[j] >> shift & 255u : 256u;
-            const uint32_t same = __match_any_sync(0xFFFFFFFFu, dig);
-            const uint32_t low = same & ((1u << lane) - 1);
-            at[j] = on ? count[warp][dig] + __popc(low) : 0;
-            __syncwarp();
-            if (on && low == 0) count[warp][dig] += __popc(same);
-            __syncwarp();
-        }
-        __syncthreads();
-        {
+        if (threadIdx.x < 256) {
             uint32_t x = base;
 #pragma unroll
             for (int w = 0; w < kSortWarps; ++w) {
-                const uint32_t c = count[w][threadIdx.x];
-                count[w][threadIdx.x] = x;
+                const uint32_t c = count[w][digit];
+                count[w][digit] = x;
                 x += c;
             }
             base = x;
         }
         __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kPerWarp / 32; ++j)
-            if (key[j] != 0xFFFFFFFFu) {
-                const uint32_t to = count[warp][key[j] >> shift & 255u] + at[j];
-                keys[to] = key[j];
-                pos[to] = from[j];
-            }
+        if (on) {
+            const uint32_t to = count[warp][dig] + __popc(low);
+            keys[to] = key;
+            pos[to] = from;
+        }
     }
 }
 

@@ -129,7 +129,7 @@ cudaError_t launch_radial_w2_tc(int64_t E, int hidden, int64_t n_out, const floa
 
 // Per-irrep norm and gated residual (norm_kernels.cuh, norm_<type>.cu).
 constexpr int kNormMaxIrreps = 32;
-constexpr int kNormForwardCtas = 152 * 8, kNormBackwardCtas = 152 * 6;
+constexpr int kNormForwardCtas = 152 * 8, kNormBackwardCtas = 152 * 8;
 struct NormIrrep {
     int l, mul, off, ch;        // first element of a row, first channel
     int T, K;                   // threads of a pair, vectors of a thread (0: read again)
@@ -143,7 +143,7 @@ struct NormTable {
 struct NormForward {
     static constexpr int kThreads = 256;  // of a CTA
     int tensors() const { return 3; }     // read a row
-    static constexpr int kCtas = kNormForwardCtas, kRowCtas = 152 * 4;
+    static constexpr int kCtas = kNormForwardCtas, kBodyCtas = kCtas, kRowCtas = 152 * 4;
     int64_t n;
     double eps;
     cgtp_rows b, x, gate, h, y;
@@ -152,7 +152,7 @@ struct NormForward {
 struct NormBackward {
     static constexpr int kThreads = 128;
     int tensors() const { return grad_y.data ? 5 : 3; }
-    static constexpr int kCtas = kNormBackwardCtas, kRowCtas = 152 * 2;
+    static constexpr int kCtas = kNormBackwardCtas, kBodyCtas = 152 * 6, kRowCtas = 152 * 2;
     int64_t n;
     double eps;
     cgtp_rows b, h, gate, grad_h, grad_y, grad_x, grad_b, grad_gate;

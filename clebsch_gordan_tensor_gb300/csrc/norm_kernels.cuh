@@ -1174,11 +1174,12 @@ norm_reduce_kernel(const __grid_constant__ NormTable tab, const __grid_constant_
 
 // ------------------------------------------------------------ launching --
 
-// T, K and the CTAs of each irrep; returns the threads of a CTA: `threads`, with
-// rows of up to that many vectors.  Plain rows may have 512 threads with up to
+// T, K and the CTAs of each irrep (of_all / all of the largest number); returns
+// the threads of a CTA: `threads`, with rows of up to that many vectors.  Plain rows may have 512 threads with up to
 // four vectors each (two of eight 16-bit channels, 16 of one).
 template <int V>
-int shape_table(NormTable& tab, int64_t n, int threads, int& most_k, int& most_l) {
+int shape_table(NormTable& tab, int64_t n, int threads, int of_all, int all, int& most_k,
+                int& most_l) {
     most_l = 0;
     for (int i = 0; i < tab.n; ++i) most_l = std::max(most_l, tab.ir[i].l);
     const bool plain = most_l == 0 && V != 8;
@@ -1203,7 +1204,8 @@ int shape_table(NormTable& tab, int64_t n, int threads, int& most_k, int& most_l
         NormIrrep& ir = tab.ir[i];
         if (ir.K == 0) ir.T = threads;
         const int64_t G = threads / ir.T;
-        ir.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(ir.max_ctas, (n + G - 1) / G));
+        const int most_ctas = std::max(1, ir.max_ctas * of_all / all);
+        ir.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(most_ctas, (n + G - 1) / G));
         ir.cta0 = tab.ctas;
         tab.ctas += ir.ctas;
     }
@@ -1344,7 +1346,7 @@ cudaError_t launch_v(NormTable tab, const Args& a, cudaStream_t s) {
         bool warp;
         if (rows_apply<S>(tab, a, threads, k, warp)) return launch_rows<S>(tab, threads, k, warp, a, s);
     }
-    const int threads = shape_table<V>(tab, a.n, Args::kThreads, k, l);
+    const int threads = shape_table<V>(tab, a.n, Args::kThreads, Args::kBodyCtas, Args::kCtas, k, l);
     constexpr int least = V > 1 ? 1 : 4;
     if (l > 3) return launch<S, V, 6, least>(tab, threads, a, s);
     // past the row kernels eight 16-bit channels leave the body that reads again

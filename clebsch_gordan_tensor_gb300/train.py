@@ -8,6 +8,8 @@ and the current torch stream; the computation runs in the library's kernels.
 from __future__ import annotations
 
 import ctypes
+import functools
+import operator
 
 import numpy as np
 import torch
@@ -25,6 +27,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 def _on():
     """The current stream's handle."""
     return _stream() if _raw_stream is None else _raw_stream(torch.cuda.current_device())
+
+
+_on_gpu = operator.attrgetter("is_cuda")
 
 
 def _at(t):
@@ -91,6 +96,13 @@ def embed_forward(index, table, scale: float = 1.0, out=None):
     return out
 
 
+@functools.lru_cache(maxsize=256)
+def _embed_workspace(ty, n, v, d) -> int:
+    nb = ctypes.c_size_t()
+    _check(lib().cgtp_embed_backward_workspace(ty, n, v, d, ctypes.byref(nb)))
+    return nb.value
+
+
 def embed_backward(index, grad_out, n_rows: int, scale: float = 1.0, out=None, workspace=None):
     """The gradient of embed_forward's table [n_rows, D]: scale times the sum of
     the rows of grad_out [N, D] at each index, zero rows where there is none.
@@ -107,9 +119,8 @@ def embed_backward(index, grad_out, n_rows: int, scale: float = 1.0, out=None, w
         _need(out, "out", grad_out.dtype, (n_rows, d))
     ty = _type(grad_out.dtype)
     if workspace is None:
-        nb = ctypes.c_size_t()
-        _check(lib().cgtp_embed_backward_workspace(ty, n, n_rows, d, ctypes.byref(nb)))
-        workspace = _scratch(nb.value, grad_out.device) if nb.value else None
+        nb = _embed_workspace(ty, n, n_rows, d)
+        workspace = _scratch(nb, grad_out.device) if nb else None
     nws = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().cgtp_embed_backward(ty, bits, n, n_rows, d, index.data_ptr(), g.data, g.stride,
                                      float(scale), out.data_ptr(), _at(workspace), nws, _on()))
@@ -304,18 +315,21 @@ class AdamW:
             for c, p in zip(self.copies, self.params):
                 c.copy_(p)
 
+    def _check_tensors(self, what, tensors, dtype):
+        if not ([t.shape for t in tensors] == self._shapes
+                and {t.dtype for t in tensors} == {dtype}
+                and all(map(_on_gpu, tensors)) and all(map(torch.Tensor.is_contiguous, tensors))):
+            raise CgtpError(f"the {what}s must be contiguous CUDA tensors of {dtype} with the "
+                            "shapes that the parameters were given with")
+
     def step(self, grads, lr=None):
         """One step for the gradients (in the order of the parameters); ``lr``
         replaces the rate for this step."""
         if len(grads) != len(self.params):
             raise CgtpError(f"{len(grads)} gradients for {len(self.params)} parameters")
         gtype, table, params = grads[0].dtype, self._table, self.params
-        for what, tensors, dtype in (("gradient", grads, gtype), ("parameter", params, self.dtype)):
-            if not ([t.shape for t in tensors] == self._shapes
-                    and {t.dtype for t in tensors} == {dtype}
-                    and all(t.is_cuda and t.is_contiguous() for t in tensors)):
-                raise CgtpError(f"the {what}s must be contiguous CUDA tensors of {dtype} with the "
-                                "shapes that the parameters were given with")
+        self._check_tensors("parameter", params, self.dtype)
+        self._check_tensors("gradient", grads, gtype)
         table[:, 0] = [p.data_ptr() for p in params]
         table[:, 1] = [g.data_ptr() for g in grads]
         args = _AdamwArgs(self.lr if lr is None else float(lr), *self.betas, self.eps,
