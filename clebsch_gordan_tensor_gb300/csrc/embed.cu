@@ -121,7 +121,9 @@ sort_count_kernel(uint32_t n, uint32_t v, uint32_t range, int shift, const I* __
                   uint32_t* __restrict__ hist, uint32_t* __restrict__ marks, uint32_t mark_words) {
     constexpr int kCopies = 8;  // of the counters, against warps that meet in one
     __shared__ uint32_t count[kCopies][256];
+    let_next_start();
     for (int i = threadIdx.x; i < kCopies * 256; i += kSortThreads) (&count[0][0])[i] = 0;
+    wait_for_previous();
     for (uint32_t i = blockIdx.x * kSortThreads + threadIdx.x; i < mark_words;
          i += gridDim.x * kSortThreads)
         marks[i] = 0;
@@ -149,6 +151,8 @@ sort_scatter_kernel(uint32_t n, uint32_t v, uint32_t range, int shift, const I* 
     __shared__ uint32_t count[kSortWarps][256];
     __shared__ uint32_t warp_sum[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, digit = threadIdx.x & 255;
+    let_next_start();
+    wait_for_previous();
     // a digit's count in all CTAs and in those before this one: a quarter of the
     // threads for every fourth CTA
     uint32_t all = 0, before = 0;
@@ -248,11 +252,13 @@ embed_sum_kernel(uint32_t n, uint32_t v, int64_t d, int T, uint32_t tiles, uint3
                  S* __restrict__ table, typename Compute<S>::type* __restrict__ partial,
                  uint32_t* __restrict__ list) {
     using C = typename Compute<S>::type;
+    let_next_start();
     const int64_t w = (int64_t)blockIdx.x * (256 / T) + threadIdx.x / T;
     const uint32_t c = (uint32_t)(w / tiles);
     const int64_t col = (w % tiles * T + threadIdx.x % T) * V;
     if (c >= chunks || col >= d) return;
     const uint32_t first = c * chunk, last = min(first + chunk, n);
+    wait_for_previous();
     uint32_t cur = keys[first];
     if (cur >= v) return;  // padding sorts last
     bool head = first > 0 && keys[first - 1] == cur;
@@ -347,6 +353,7 @@ embed_join_kernel(uint32_t v, int64_t d, int T, uint32_t tiles, uint32_t chunk, 
     __shared__ C part[8][32 * V];
     __shared__ uint32_t run_c[8], run_rows[8], run_key[8], run_tile[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    wait_for_previous();
     if (blockIdx.x >= join_ctas) {
         const uint32_t warps = (gridDim.x - join_ctas) * 8;
         Pack<S, V> zero;
@@ -590,14 +597,22 @@ cudaError_t sort_pass(const EmbedCall& c, const Layout& L, int shift, const I* i
     const uint32_t n = (uint32_t)c.n, v = (uint32_t)c.v;
     const bool first = pos_in == nullptr;
     const uint32_t words = first ? (uint32_t)((L.list - L.marks) / 4 + 1) : 0;
-    sort_count_kernel<I><<<L.sort_ctas, kSortThreads, 0, s>>>(
-        n, v, L.range, shift, in, hist, (uint32_t*)(ws + L.marks), words);
-    sort_scatter_kernel<I><<<L.sort_ctas, kSortThreads, 0, s>>>(
-        n, v, L.range, shift, in, pos_in, hist, (uint32_t*)(ws + L.keys[to]),
-        (uint32_t*)(ws + L.pos[to]));
+    uint32_t* marks = (uint32_t*)(ws + L.marks);
+    cudaError_t e;
+    if (first) {  // after all that is on the stream
+        sort_count_kernel<I><<<L.sort_ctas, kSortThreads, 0, s>>>(n, v, L.range, shift, in, hist,
+                                                                  marks, words);
+        e = cudaGetLastError();
+    } else {
+        e = launch_chained(sort_count_kernel<I>, L.sort_ctas, kSortThreads, s, n, v, L.range, shift,
+                           in, hist, marks, words);
+    }
     count_launch();
+    if (e != cudaSuccess) return e;
     count_launch();
-    return cudaGetLastError();
+    return launch_chained(sort_scatter_kernel<I>, L.sort_ctas, kSortThreads, s, n, v, L.range,
+                          shift, in, pos_in, hist, (uint32_t*)(ws + L.keys[to]),
+                          (uint32_t*)(ws + L.pos[to]));
 }
 
 // V: elements of an access; J: sums of one in the join.
@@ -610,22 +625,21 @@ cudaError_t backward_v(const EmbedCall& c, const Layout& L, int sorted, cudaStre
     uint32_t* list = (uint32_t*)(ws + L.list);
     const int T = lanes_for((c.d + V - 1) / V);
     const uint32_t tiles = (uint32_t)((c.d + (int64_t)T * V - 1) / ((int64_t)T * V));
-    embed_sum_kernel<S, V><<<blocks_for((int64_t)L.chunks * tiles, T), 256, 0, s>>>(
-        (uint32_t)c.n, (uint32_t)c.v, c.d, T, tiles, L.chunk, L.chunks, keys, pos, ws + L.marks,
-        (const S*)c.in, c.in_stride, (C)c.scale, (S*)c.out, (C*)(ws + L.partial), list);
+    cudaError_t e = launch_chained(
+        embed_sum_kernel<S, V>, blocks_for((int64_t)L.chunks * tiles, T), 256, s, (uint32_t)c.n,
+        (uint32_t)c.v, c.d, T, tiles, L.chunk, L.chunks, keys, pos, ws + L.marks, (const S*)c.in,
+        c.in_stride, (C)c.scale, (S*)c.out, (C*)(ws + L.partial), list);
     count_launch();
-    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int TJ = lanes_for((c.d + J - 1) / J);
     const uint32_t join_tiles = (uint32_t)((c.d + (int64_t)TJ * J - 1) / ((int64_t)TJ * J));
     const uint32_t joins =
         (uint32_t)std::min<int64_t>(((int64_t)L.chunks * join_tiles + 7) / 8, 152 * 6);
     const uint32_t zeros = (uint32_t)std::min<int64_t>((c.v + 7) / 8, 152 * 2);
-    embed_join_kernel<S, J><<<joins + zeros, 256, 0, s>>>(
-        (uint32_t)c.v, c.d, TJ, join_tiles, L.chunk, L.chunks, joins, keys, ws + L.marks,
-        (C)c.scale, (S*)c.out, (const C*)(ws + L.partial), list);
     count_launch();
-    return cudaGetLastError();
+    return launch_chained(embed_join_kernel<S, J>, joins + zeros, 256, s, (uint32_t)c.v, c.d, TJ,
+                          join_tiles, L.chunk, L.chunks, joins, keys, ws + L.marks, (C)c.scale,
+                          (S*)c.out, (const C*)(ws + L.partial), list);
 }
 
 // Rows that can move in 16-byte accesses.

@@ -603,6 +603,7 @@ __device__ __forceinline__ void backward_body(const NormIrrep& ir, int cta, cons
     }
     if constexpr (kRing) copies_wait<0>();
     if (!a.partial) return;
+    let_next_start();
     // The groups' sums, added in group order through shared memory.
     C* rows = reinterpret_cast<C*>(dynamic);
     C* out = partial_row<C>(ir, cta, a);
@@ -1112,6 +1113,7 @@ row_backward_kernel(const __grid_constant__ NormTable tab, const __grid_constant
     }
     copies_wait<0>();
     if (!a.partial) return;
+    let_next_start();
     C* out = partial_row<C>(ir, cta, a);
     // The groups' sums, added in group order through shared memory.
     C* rows = reinterpret_cast<C*>(dynamic);
@@ -1148,6 +1150,7 @@ norm_reduce_kernel(const __grid_constant__ NormTable tab, const __grid_constant_
     __shared__ C part[32][32];
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), lane = threadIdx.x >> 5;
     const int which = blockIdx.y;
+    wait_for_previous();
     C s = 0;
     if (col < a.channels) {
         int i = 0;
@@ -1231,9 +1234,9 @@ cudaError_t finish(const NormTable&, const NormForward&, cudaStream_t) {
 template <typename C>
 cudaError_t finish(const NormTable& tab, const NormBackward& a, cudaStream_t s) {
     if (!a.partial) return cudaSuccess;
-    norm_reduce_kernel<C><<<dim3((unsigned)((a.channels + 31) / 32), 2), 1024, 0, s>>>(tab, a);
     count_launch();
-    return cudaGetLastError();
+    return launch_chained(norm_reduce_kernel<C>, dim3((unsigned)((a.channels + 31) / 32), 2), 1024,
+                          s, tab, a);
 }
 
 template <typename S, int V, int LC, int K>
