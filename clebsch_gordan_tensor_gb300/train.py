@@ -22,14 +22,15 @@ _NONE = _Rows(None, 0)
 # The small calls here are as long as their Python: the raw stream spares a
 # Stream object a call.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _on():
     """The current stream's handle."""
-    return _stream() if _raw_stream is None else _raw_stream(torch.cuda.current_device())
+    return _stream() if _raw_stream is None else _raw_stream(_device())
 
 
-_on_gpu = operator.attrgetter("is_cuda")
+_facts = operator.attrgetter("shape", "dtype", "is_cuda")
 
 
 def _at(t):
@@ -179,7 +180,7 @@ class IrrepsNorm:
 
     def _new(self, like, n, width):
         """New rows, and their description."""
-        t = torch.empty((n, width), dtype=self.dtype, device=like.device)
+        t = like.new_empty((n, width))
         return t, _Rows(t.data_ptr(), width)
 
     def _space(self, workspace, device):
@@ -295,6 +296,7 @@ class AdamW:
         # cgtp_adamw_tensor rows: parameter, gradient, length; filled in by step()
         self._table = np.zeros((n, 3), dtype=np.int64)
         self._shapes = [p.shape for p in self.params]
+        self._want = {}  # what a step expects of its tensors, by dtype
         self._table[:, 2] = [p.numel() for p in self.params]
         numel = (ctypes.c_int64 * n)(*self._table[:, 2].tolist())
         first, total = (ctypes.c_int64 * n)(), ctypes.c_int64()
@@ -316,9 +318,10 @@ class AdamW:
                 c.copy_(p)
 
     def _check_tensors(self, what, tensors, dtype):
-        if not ([t.shape for t in tensors] == self._shapes
-                and {t.dtype for t in tensors} == {dtype}
-                and all(map(_on_gpu, tensors)) and all(map(torch.Tensor.is_contiguous, tensors))):
+        want = self._want.get(dtype)
+        if want is None:
+            want = self._want[dtype] = [(shape, dtype, True) for shape in self._shapes]
+        if list(map(_facts, tensors)) != want or not all(map(torch.Tensor.is_contiguous, tensors)):
             raise CgtpError(f"the {what}s must be contiguous CUDA tensors of {dtype} with the "
                             "shapes that the parameters were given with")
 
@@ -330,8 +333,8 @@ class AdamW:
         gtype, table, params = grads[0].dtype, self._table, self.params
         self._check_tensors("parameter", params, self.dtype)
         self._check_tensors("gradient", grads, gtype)
-        table[:, 0] = [p.data_ptr() for p in params]
-        table[:, 1] = [g.data_ptr() for g in grads]
+        table[:, 0] = list(map(torch.Tensor.data_ptr, params))
+        table[:, 1] = list(map(torch.Tensor.data_ptr, grads))
         args = _AdamwArgs(self.lr if lr is None else float(lr), *self.betas, self.eps,
                           self.weight_decay, self.step_count + 1, self.seed)
         _check(lib().cgtp_adamw_step(_type(self.dtype), _type(gtype), self.state_bits, len(grads),
