@@ -1,8 +1,8 @@
 """Clebsch-Gordan tensor products on GB300 (sm_103a): Python binding.
 
-A thin ctypes layer over the C ABI of ``libcgtp.so`` (declared in
-``include/cgtp.h``).  It marshals torch CUDA tensors into pointers and the
-current torch stream; every step of the computation runs in the library's own
+A thin layer over the C ABI of ``libcgtp.so`` (declared in ``include/cgtp.h``),
+by ctypes here and natively for the training operators (``train.py``).  It
+marshals torch CUDA tensors into pointers and the current torch stream; every step of the computation runs in the library's own
 kernels.  If the library has not been built, every entry point raises -- there
 is no CPU fallback.
 

@@ -1,5 +1,6 @@
 """Build libcgtp.so in-tree: host C++ with g++, fixed kernels with nvcc for
-sm_103a, the tensor-product kernel template embedded as a string for NVRTC.
+sm_103a, the tensor-product kernel template embedded as a string for NVRTC; and
+cgtp_binding.so, the native marshalling of the training operators.
 
 Run ``python -m clebsch_gordan_tensor_gb300.build`` or call ``build()``.
 Translation units compile in parallel; nothing is rebuilt when up to date.
@@ -16,6 +17,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libcgtp.so")
+BINDING = os.path.join(OUT, "cgtp_binding.so")
 CUDA = os.environ.get("CUDA_HOME", "/usr/local/cuda")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -37,6 +39,26 @@ def _stale(obj: str, deps) -> bool:
         return True
     t = os.path.getmtime(obj)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _torch():
+    """Include and library directories of the native binding."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include")]
+    return [f for d in inc for f in ("-I", d)], os.path.join(root, "lib")
+
+
+def _link(out: str, objs, flags) -> None:
+    tmp = out + f".{os.getpid()}.tmp"
+    cmd = ["g++", "-shared", "-o", tmp, *objs, *flags]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stderr}")
+    os.replace(tmp, out)
 
 
 def build(verbose: bool = False) -> str:
@@ -65,6 +87,13 @@ def build(verbose: bool = False) -> str:
                "-Xcompiler", "-fPIC", *inc, "-c", src, "-o", obj]
         jobs.append((obj, [src, *headers], cmd))
 
+    torch_inc, torch_lib = _torch()
+    src = os.path.join(CSRC, "binding.cpp")
+    binding = os.path.join(OUT, "binding.cpp.o")
+    jobs.append((binding, [src, headers[0]],
+                 ["g++", "-std=c++17", "-O2", "-fPIC", "-Wall", *inc, *torch_inc, "-c", src, "-o",
+                  binding]))
+
     def run(job):
         obj, deps, cmd = job
         if not _stale(obj, deps):
@@ -80,15 +109,13 @@ def build(verbose: bool = False) -> str:
         errs = [e for e in ex.map(run, jobs) if e]
     if errs:
         raise RuntimeError("build failed:\n" + "\n".join(errs))
-    objs = [j[0] for j in jobs]
+    objs = [j[0] for j in jobs if j[0] != binding]
     if _stale(LIB, objs):
-        tmp = LIB + f".{os.getpid()}.tmp"
-        cmd = ["g++", "-shared", "-o", tmp, *objs, "-L", os.path.join(CUDA, "lib64"),
-               "-lcudart", "-lnvrtc", f"-Wl,-rpath,{os.path.join(CUDA, 'lib64')}"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stderr}")
-        os.replace(tmp, LIB)
+        _link(LIB, objs, ["-L", os.path.join(CUDA, "lib64"), "-lcudart", "-lnvrtc",
+                          f"-Wl,-rpath,{os.path.join(CUDA, 'lib64')}"])
+    if _stale(BINDING, [binding]):
+        _link(BINDING, [binding], ["-L", OUT, "-lcgtp", "-L", torch_lib, "-lc10", "-lc10_cuda",
+                                   "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"])
     return LIB
 
 

