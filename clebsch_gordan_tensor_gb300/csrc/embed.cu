@@ -246,16 +246,17 @@ __device__ __forceinline__ void store_sums(C* p, const C (&x)[V]) {
 
 constexpr int kSumCtas = 3;  // resident on an SM
 
-// One group of T lanes: the runs of chunk c in the columns of one tile.  Marks
-// the rows that it meets.
+// One group of T lanes: the runs of chunk c in the columns of one tile.  Marks a
+// row with the chunk (plus one) in which its run ends, and lists the runs that
+// start in the chunk and go on, as (chunk, row).
 template <typename S, int V>
 __global__ void __launch_bounds__(256, kSumCtas)
 embed_sum_kernel(uint32_t n, uint32_t v, int64_t d, int T, uint32_t tiles, uint32_t chunk,
                  uint32_t chunks, const uint32_t* __restrict__ keys,
-                 const uint32_t* __restrict__ pos, uint8_t* __restrict__ marks,
+                 const uint32_t* __restrict__ pos, uint32_t* __restrict__ marks,
                  const S* __restrict__ g, int64_t stride, typename Compute<S>::type scale,
                  S* __restrict__ table, typename Compute<S>::type* __restrict__ partial,
-                 uint32_t* __restrict__ list) {
+                 uint2* __restrict__ list) {
     using C = typename Compute<S>::type;
     let_next_start();
     const int64_t w = (int64_t)blockIdx.x * (256 / T) + threadIdx.x / T;
@@ -270,8 +271,8 @@ embed_sum_kernel(uint32_t n, uint32_t v, int64_t d, int T, uint32_t tiles, uint3
     C acc[V] = {};
     auto finish = [&](bool tail) {
         if (col == 0) {
-            marks[cur] = 1;
-            if (tail && !head) list[1 + atomicAdd(list, 1u)] = c;  // joined in any order
+            if (!tail) marks[cur] = c + 1;
+            if (tail && !head) list[1 + atomicAdd(&list->x, 1u)] = make_uint2(c, cur);
         }
         if (head || tail) {
             store_sums(partial + ((int64_t)c * 2 + (head ? 0 : 1)) * d + col, acc);
@@ -326,17 +327,18 @@ embed_sum_kernel(uint32_t n, uint32_t v, int64_t d, int T, uint32_t tiles, uint3
 template <typename C, int V>
 __device__ __forceinline__ void add_run(C (&acc)[V], const C* partial, int64_t d, int64_t col,
                                         uint32_t c, uint32_t from, uint32_t to) {
-    for (uint32_t first = from; first < to; first += 8) {
-        Pack<C, V> x[8];
+    constexpr int U = 16;  // rows in flight
+    for (uint32_t first = from; first < to; first += U) {
+        Pack<C, V> x[U];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < U; ++j) {
             const uint32_t i = first + j;
             x[j].fill(0);
             if (i < to)
                 x[j] = load_pack<C, V>(partial + ((int64_t)(c + i) * 2 + (i == 0 ? 1 : 0)) * d + col);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < U; ++j)
 #pragma unroll
             for (int k = 0; k < V; ++k) acc[k] += x[j].v[k];
     }
@@ -348,15 +350,15 @@ __device__ __forceinline__ void add_run(C (&acc)[V], const C* partial, int64_t d
 // then added in order.  CTAs past join_ctas zero the rows without a mark.
 template <typename S, int V>
 __global__ void __launch_bounds__(256)
-embed_join_kernel(uint32_t v, int64_t d, int T, uint32_t tiles, uint32_t chunk, uint32_t chunks,
-                  uint32_t join_ctas, const uint32_t* __restrict__ keys,
-                  const uint8_t* __restrict__ marks, typename Compute<S>::type scale,
+embed_join_kernel(uint32_t v, int64_t d, int T, uint32_t tiles, uint32_t join_ctas,
+                  const uint32_t* __restrict__ marks, typename Compute<S>::type scale,
                   S* __restrict__ table, const typename Compute<S>::type* __restrict__ partial,
-                  const uint32_t* __restrict__ list) {
+                  const uint2* __restrict__ list) {
     using C = typename Compute<S>::type;
     constexpr uint32_t kLong = 32;  // chunks: above it, eight warps
     __shared__ C part[8][32 * V];
-    __shared__ uint32_t run_c[8], run_rows[8], run_key[8], run_tile[8];
+    __shared__ uint2 run[8];
+    __shared__ uint32_t run_rows[8], run_tile[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     wait_for_previous();
     if (blockIdx.x >= join_ctas) {
@@ -369,14 +371,14 @@ embed_join_kernel(uint32_t v, int64_t d, int T, uint32_t tiles, uint32_t chunk, 
                     store_pack(table + (int64_t)r * d + c, zero);
         return;
     }
-    const uint64_t items = (uint64_t)list[0] * tiles;
+    const uint64_t items = (uint64_t)list->x * tiles;
     const int t = lane % T, shares = 32 / T;
-    auto write = [&](C (&acc)[V], uint32_t cur, int64_t col) {
+    auto write = [&](C (&acc)[V], uint32_t row, int64_t col) {
         Pack<S, V> o;
 #pragma unroll
         for (int k = 0; k < V; ++k) acc[k] *= scale;
         o.set(acc);
-        store_pack(table + (int64_t)cur * d + col, o);
+        store_pack(table + (int64_t)row * d + col, o);
     };
     // a share of a warp's lanes each, added in order; the result in share 0
     auto add_shares = [&](C (&acc)[V]) {
@@ -392,41 +394,19 @@ embed_join_kernel(uint32_t v, int64_t d, int T, uint32_t tiles, uint32_t chunk, 
         const uint64_t item = base + (uint64_t)warp * join_ctas;
         uint32_t rows = 0;
         if (item < items) {
-            const uint32_t c = list[1 + item / tiles];
-            const uint32_t cur = keys[(int64_t)(c + 1) * chunk];  // the run goes on there
-            // the first chunk not to start with it, among the next 32, then by
-            // 32 probes at a time in what is left
-            uint32_t lo = c + 2, hi = min(lo + 32, chunks);
-            for (bool near = true;; near = false) {
-                const uint32_t step = (hi - lo + 31) / 32, at = lo + lane * step;
-                const bool go = at < hi && keys[(int64_t)at * chunk] == cur;
-                const uint32_t miss = ~__ballot_sync(0xFFFFFFFFu, go);
-                const uint32_t on = miss ? __ffs(miss) - 1 : 32;  // probes that go on
-                if (near && on == 32 && hi < chunks) {
-                    lo = hi, hi = chunks;
-                    continue;
-                }
-                if (step <= 1) {
-                    lo = min(lo + on, hi);
-                    break;
-                }
-                hi = min(lo + on * step, hi);  // misses here, or the end
-                lo = on ? lo + (on - 1) * step + 1 : lo;
-                if (on == 0) break;
-            }
-            rows = lo - c;
+            const uint2 r = list[1 + item / tiles];
+            rows = marks[r.y] - r.x;  // one a chunk, from its start to its end
             if (rows <= kLong) {
                 const uint32_t share = (rows + shares - 1) / shares;
                 const uint32_t from = min(lane / T * share, rows), to = min(from + share, rows);
                 const int64_t col = ((int64_t)(item % tiles) * T + t) * V;
                 C acc[V] = {};
-                if (col < d) add_run(acc, partial, d, col, c, from, to);
+                if (col < d) add_run(acc, partial, d, col, r.x, from, to);
                 add_shares(acc);
-                if (lane < T && col < d) write(acc, cur, col);
+                if (lane < T && col < d) write(acc, r.y, col);
             }
             if (lane == 0) {
-                run_c[warp] = c;
-                run_key[warp] = cur;
+                run[warp] = r;
                 run_tile[warp] = (uint32_t)(item % tiles);
             }
         }
@@ -439,8 +419,7 @@ embed_join_kernel(uint32_t v, int64_t d, int T, uint32_t tiles, uint32_t chunk, 
             const uint32_t from = min((warp * shares + lane / T) * share, all);
             const int64_t col = ((int64_t)run_tile[r] * T + t) * V;
             C acc[V] = {};
-            if (col < d)
-                add_run(acc, partial, d, col, run_c[r], from, min(from + share, all));
+            if (col < d) add_run(acc, partial, d, col, run[r].x, from, min(from + share, all));
             add_shares(acc);
 #pragma unroll
             for (int k = 0; k < V; ++k) part[warp][lane * V + k] = acc[k];
@@ -449,7 +428,7 @@ embed_join_kernel(uint32_t v, int64_t d, int T, uint32_t tiles, uint32_t chunk, 
                 for (int w = 1; w < 8; ++w)
 #pragma unroll
                     for (int k = 0; k < V; ++k) acc[k] += part[w][lane * V + k];
-                write(acc, run_key[r], col);
+                write(acc, run[r].y, col);
             }
             __syncthreads();
         }
@@ -586,8 +565,8 @@ Layout layout_of(cgtp_dtype type, int64_t n, int64_t v, int64_t d) {
     }
     L.hist = at, at += up256((size_t)L.sort_ctas * 256 * 4);
     // cleared together: the marks, then the list's length
-    L.marks = at, at += ((size_t)v + 3) / 4 * 4;
-    L.list = at, at = up256(at + ((size_t)L.chunks + 1) * 4);
+    L.marks = at, at += ((size_t)v + 1) / 2 * 8;
+    L.list = at, at = up256(at + ((size_t)L.chunks + 1) * 8);
     L.partial = at;
     at += up256((size_t)L.chunks * 2 * (size_t)d * (type == CGTP_F64 ? 8 : 4));
     L.total = at;
@@ -627,12 +606,13 @@ cudaError_t backward_v(const EmbedCall& c, const Layout& L, int sorted, cudaStre
     uint8_t* ws = (uint8_t*)c.ws;
     const uint32_t* keys = (const uint32_t*)(ws + L.keys[sorted]);
     const uint32_t* pos = (const uint32_t*)(ws + L.pos[sorted]);
-    uint32_t* list = (uint32_t*)(ws + L.list);
+    uint2* list = (uint2*)(ws + L.list);
+    uint32_t* marks = (uint32_t*)(ws + L.marks);
     const int T = lanes_for((c.d + V - 1) / V);
     const uint32_t tiles = (uint32_t)((c.d + (int64_t)T * V - 1) / ((int64_t)T * V));
     cudaError_t e = launch_chained(
         embed_sum_kernel<S, V>, blocks_for((int64_t)L.chunks * tiles, T), 256, s, (uint32_t)c.n,
-        (uint32_t)c.v, c.d, T, tiles, L.chunk, L.chunks, keys, pos, ws + L.marks, (const S*)c.in,
+        (uint32_t)c.v, c.d, T, tiles, L.chunk, L.chunks, keys, pos, marks, (const S*)c.in,
         c.in_stride, (C)c.scale, (S*)c.out, (C*)(ws + L.partial), list);
     count_launch();
     if (e != cudaSuccess) return e;
@@ -643,8 +623,8 @@ cudaError_t backward_v(const EmbedCall& c, const Layout& L, int sorted, cudaStre
     const uint32_t zeros = (uint32_t)std::min<int64_t>((c.v + 7) / 8, 152 * 2);
     count_launch();
     return launch_chained(embed_join_kernel<S, J>, joins + zeros, 256, s, (uint32_t)c.v, c.d, TJ,
-                          join_tiles, L.chunk, L.chunks, joins, keys, ws + L.marks, (C)c.scale,
-                          (S*)c.out, (const C*)(ws + L.partial), list);
+                          join_tiles, joins, marks, (C)c.scale, (S*)c.out,
+                          (const C*)(ws + L.partial), list);
 }
 
 // Rows that can move in 16-byte accesses.
@@ -667,14 +647,13 @@ cudaError_t small_v(const EmbedCall& c, cudaStream_t s) {
 
 // Whether the gradient takes one launch, with vectors of V elements: few indices,
 // and not so many rows and tiles of columns that each scans all of them for.
-// The time of that kernel goes by the CTAs times the indices and a constant: up
-// to 5 million it matched the sorted form's or beat it (1024 indices, 119 x 64
-// fp32: 24.0 us and 24.2 us in four launches; 16,000 x 512 bf16: 32.0 and 32.3 us
-// in six; 200 indices, 50,000 x 256 fp32: 31.6 and 39.8 us), at 39 million it lost
-// (1024 indices, 32,000 x 2048 bf16: 215 and 52 us).
+// That kernel's time goes by the CTAs times the indices and a constant.  One
+// launch and the sorted form, in us: 8.2 and 18.0 at 0.3 million (1024 indices,
+// 1000 x 256 fp32), 12.4 and 18.0 at 1.4 (500, 8000 x 256), 30.6 and 27.5 at 3.3 (64,
+// 50,000 x 512 bf16), 31.2 and 22.3 at 4.9 (1024, 16,000 x 512 bf16).
 bool small(int64_t n, int64_t v, int64_t d, int64_t V) {
     const int64_t tiles = (d + 32 * V - 1) / (32 * V);
-    return n <= kSmallN && tiles <= 65535 && (v + 7) / 8 * tiles <= 5000000 / (n + 200);
+    return n <= kSmallN && tiles <= 65535 && (v + 7) / 8 * tiles <= 2000000 / (n + 200);
 }
 
 template <typename S>

@@ -482,6 +482,114 @@ def test_adamw_states_resume_to_the_bit():
         assert all(torch.equal(x, y) for x, y in zip(a, b)) and torch.equal(one.m, two.m)
 
 
+# ---------------------------------------------- past 2^31 and 2^32 elements --
+
+
+def _room(gb):
+    if torch.cuda.mem_get_info()[0] < gb * 2 ** 30:
+        pytest.skip(f"needs {gb} GB of device memory")
+
+
+def test_embed_past_32_bit_offsets():
+    cg = _cg()
+    _room(24)
+    n, v, d = 2_200_000, 9, 1000  # 2.2e9 elements of bfloat16
+    idx = torch.arange(n, device="cuda", dtype=torch.int32) % v
+    table = torch.randn(v, d, device="cuda").bfloat16()
+    out = cg.embed_forward(idx, table)
+    for at in (0, n // 2, n - 3):
+        assert torch.equal(out[at:at + 3], table[idx[at:at + 3].long()])
+    out.zero_()
+    out[-5:] = table[:5]  # only the last rows count
+    got = cg.embed_backward(idx, out, v)
+    ref = torch.zeros_like(table)
+    ref[idx[-5:].long()] = table[:5]
+    assert torch.equal(got, ref)
+
+
+def test_norm_past_32_bit_offsets():
+    cg = _cg()
+    _room(40)
+    irreps, n = "8x0e+8x1o", 70_000_000  # 2.24e9 elements of bfloat16
+    norm = cg.IrrepsNorm(irreps, dtype=BF16)
+    x = torch.zeros(n, 32, dtype=BF16, device="cuda")
+    x[-4:] = torch.randn(4, 32, device="cuda")
+    y = norm.forward(x)
+    R.assert_rounded(y[-4:], R.norm(x[-4:].cpu().double(), None, irreps, 1e-5), BF16, "y")
+    assert (y[:1000] == 0).all()
+    g = torch.zeros_like(x)
+    g[-4:] = torch.randn(4, 32, device="cuda")
+    gx, gw = norm.backward(x, g)
+    leaf = x[-4:].cpu().double().requires_grad_()
+    w = torch.ones(16, dtype=F64, requires_grad=True)
+    rx, rw = torch.autograd.grad(R.norm(leaf, w, irreps, 1e-5), (leaf, w), g[-4:].cpu().double())
+    R.assert_rounded(gx[-4:], rx, BF16, "grad_x")
+    R.assert_rounded(gw, rw, F32, "grad_weight")
+
+
+def test_adamw_past_32_bit_offsets():
+    """More than 2^32 elements in one tensor: the last block's codes, whose hash
+    takes the element's upper half too."""
+    cg = _cg()
+    _room(48)
+    n = 2 ** 32 + 300
+    p = torch.zeros(n, dtype=BF16, device="cuda")
+    g = torch.zeros(n, dtype=BF16, device="cuda")
+    g[-300:] = torch.randn(300, device="cuda")
+    opt = cg.AdamW([p], state_bits=8, seed=11, **HYPER)
+    opt.step([g])
+    gs = _np(g[-300:]).astype(np.float32)
+    f = np.float32
+    m, v = gs * f(1 - 0.9), (gs * gs) * f(1 - 0.99)
+    key = R.mix32(R.mix32(R.mix32(11) ^ 0) + 1)
+    key = R.mix32(R.mix32(key + 0) + 1)  # of tensor 0, upper half 1
+    h = [R.mix32(k ^ key) for k in range(300)]
+    um = np.array([(x >> 16) + 0.5 for x in h]) / 65536
+    uv = np.array([(x & 0xFFFF) + 0.5 for x in h]) / 65536
+    cm, xm = R.encode(R.pad256(m), 4, R.pad256(um))
+    cv, xv = R.encode(R.pad256(v), 5, R.pad256(uv))
+    assert np.array_equal(opt.m[-512:].cpu().numpy(), cm)
+    assert np.array_equal(opt.v[-512:].cpu().numpy(), cv)
+    assert np.array_equal(opt.m_exp[-2:].cpu().numpy(), xm)
+    assert np.array_equal(opt.v_exp[-2:].cpu().numpy(), xv)
+    assert (p[:1000] == 0).all() and (p[-300:] != 0).all()
+
+
+# --------------------------------------------------------- captured graphs --
+
+
+def test_calls_in_a_captured_graph():
+    """Chained launches and workspaces from the graph's pool: replays follow their
+    inputs."""
+    cg = _cg()
+    gen = torch.Generator().manual_seed(4)
+    norm = cg.IrrepsNorm("16x0e+16x1o")
+    idx = _index(5000, 60, torch.int32, 3)
+    x, b, gh, gy = (_rows(gen, 500, 64, F32) for _ in range(4))
+    table, g = _rows(gen, 60, 40, F32), _rows(gen, 5000, 40, F32)
+
+    def work():
+        h, y = norm.residual_forward(x, b)
+        return [cg.embed_forward(idx, table), cg.embed_backward(idx, g, 60), h, y,
+                *(t for t in norm.residual_backward(b, h, gh, gy) if t is not None)]
+
+    work()  # kernels load before the capture
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = work()
+    for k in range(3):
+        for t in (x, b, gh, gy, table, g):
+            t.copy_(torch.randn(t.shape, generator=gen))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, e) for a, e in zip(got, work())), k
+
+
 # ------------------------------------------------------- streams, refusals --
 
 def test_calls_follow_the_current_stream():
