@@ -59,6 +59,7 @@ struct AdamwTable {
 template <typename C>
 struct AdamwScalars {
     C b1, c1, b2, c2, keep, rate, root, eps;
+    uint32_t s16, s13, s20, s12;
 };
 
 // Finaliser of MurmurHash3's 32-bit variant (A. Appleby, public domain).
@@ -102,8 +103,9 @@ __device__ __forceinline__ Two<float> decode_v(uint32_t four, int i, Two<float> 
 }
 // y, the fp32 bits of a scaled magnitude, with the noise below the last bit kept
 // added: the code, but for the clamp at the largest one.
-__device__ __forceinline__ int rounded(float y, uint32_t noise) {
-    return (int)((__float_as_uint(y) + noise) >> 20);
+__device__ __forceinline__ uint32_t shr(uint32_t x, uint32_t by);
+__device__ __forceinline__ int rounded(float y, uint32_t noise, uint32_t by) {
+    return (int)shr(__float_as_uint(y) + noise, by);
 }
 // Four codes, clamped to a signed (127) or unsigned (255) byte, first one lowest.
 __device__ __forceinline__ uint32_t pack_s8(int a, int b, int c, int d) {
@@ -135,6 +137,14 @@ __device__ __forceinline__ uint32_t signs(Two<float> a, Two<float> b) {
 __device__ __forceinline__ float larger(float top, float x) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(top), "f"(fabsf(x)));
+    return r;
+}
+
+// x >> (32 - log2 by) on the multiply pipe: by is a power of two that the compiler
+// does not know.
+__device__ __forceinline__ uint32_t shr(uint32_t x, uint32_t by) {
+    uint32_t r;
+    asm("mul.hi.u32 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(by));
     return r;
 }
 
@@ -174,7 +184,7 @@ __device__ __forceinline__ Two<double> stepped(Two<double> p, Two<double> m, Two
 
 // copy_kind: 0 none, 1 bfloat16, 2 binary16.
 template <typename P, typename G, bool EIGHT>
-__global__ void __launch_bounds__(32 * kWarps, EIGHT ? 5 : 1)
+__global__ void __launch_bounds__(32 * kWarps, EIGHT ? 4 : 1)
 adamw_kernel(const __grid_constant__ AdamwTable tab,
              const AdamwScalars<typename Compute<P>::type> a, void* __restrict__ m_,
              void* __restrict__ v_, uint8_t* __restrict__ m_exp, uint8_t* __restrict__ v_exp,
@@ -185,22 +195,75 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
     constexpr int H = V / 2;
     const int lane = threadIdx.x & 31;
     const uint32_t warps = gridDim.x * kWarps;
+    // 8-bit states leave the kernel more arithmetic than its loads can wait for:
+    // the next block's rows are on their way through shared memory meanwhile,
+    // each lane copying what it reads itself.
+    __shared__ Pack<P, V> next_p[EIGHT ? NV : 1][EIGHT ? 32 * kWarps : 1];
+    __shared__ Pack<G, V> next_g[EIGHT ? NV : 1][EIGHT ? 32 * kWarps : 1];
+    __shared__ uint32_t next_m[EIGHT ? NV : 1][EIGHT ? 32 * kWarps : 1];
+    __shared__ uint32_t next_v[EIGHT ? NV : 1][EIGHT ? 32 * kWarps : 1];
+    const int tid = EIGHT ? threadIdx.x : 0;
+    struct Where {
+        P* p;
+        const G* g;
+        int64_t first, left;
+        uint32_t key;
+        bool whole;  // a full block that vectors can move
+        uint8_t m_exp, v_exp;
+    };
     int lo = 0;  // the block's tensor: the last one that starts at or before it
-    for (uint32_t b = blockIdx.x * kWarps + (threadIdx.x >> 5); b < tab.blocks; b += warps) {
+    auto find = [&](uint32_t b) {
         while (lo + 1 < tab.n && tab.t[lo + 1].block0 <= b) ++lo;
         const AdamwEntry& e = tab.t[lo];
-        const int64_t first = (int64_t)(b - e.block0) * kBlock;
-        const int64_t left = e.numel - first, at = (int64_t)b * kBlock;
-        P* const p = static_cast<P*>(e.p) + first;
-        const G* const g = static_cast<const G*>(e.g) + first;
-        const bool whole = left >= kBlock && e.vectors;
+        Where w;
+        w.first = (int64_t)(b - e.block0) * kBlock;
+        w.left = e.numel - w.first;
+        w.p = static_cast<P*>(e.p) + w.first;
+        w.g = static_cast<const G*>(e.g) + w.first;
+        w.whole = w.left >= kBlock && e.vectors;
+        w.key = e.key;
+        if constexpr (EIGHT) {
+            w.m_exp = m_exp[b];
+            w.v_exp = v_exp[b];
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int64_t k = (int64_t)b * kBlock + (j * 32 + lane) * V;
+                copy_async<4>(&next_m[j][tid], (uint8_t*)m_ + k);
+                copy_async<4>(&next_v[j][tid], (uint8_t*)v_ + k);
+                if (w.whole) {
+                    copy_async<sizeof(P) * V>(&next_p[j][tid], w.p + (j * 32 + lane) * V);
+                    copy_async<sizeof(G) * V>(&next_g[j][tid], w.g + (j * 32 + lane) * V);
+                }
+            }
+            copies_end_group();
+        }
+        return w;
+    };
+    uint32_t b = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (b >= tab.blocks) return;
+    for (Where next = find(b); b < tab.blocks;) {
+        const Where e = next;
+        P* const p = e.p;
+        const G* const g = e.g;
+        const int64_t left = e.left, at = (int64_t)b * kBlock;
+        const bool whole = e.whole;
+        const uint32_t block = b;
+        b += warps;
         C pn[NV][V], gg[NV][V];
         Two<C> m[NV][H], v[NV][H];
+        if constexpr (EIGHT) copies_wait<0>();
         if (whole) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const Pack<P, V> pp = load_pack<P, V>(p + (j * 32 + lane) * V);
-                const Pack<G, V> gp = load_pack<G, V>(g + (j * 32 + lane) * V);
+                Pack<P, V> pp;
+                Pack<G, V> gp;
+                if constexpr (EIGHT) {
+                    pp = next_p[j][tid];
+                    gp = next_g[j][tid];
+                } else {
+                    pp = load_pack<P, V>(p + (j * 32 + lane) * V);
+                    gp = load_pack<G, V>(g + (j * 32 + lane) * V);
+                }
 #pragma unroll
                 for (int i = 0; i < V; ++i) pn[j][i] = pp.get(i), gg[j][i] = (C)gp.get(i);
             }
@@ -215,12 +278,10 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
                 }
         }
         if constexpr (EIGHT) {
-            const float ms = block_scale(m_exp[b]), vs = block_scale(v_exp[b]);
+            const float ms = block_scale(e.m_exp), vs = block_scale(e.v_exp);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int64_t k = at + (j * 32 + lane) * V;
-                const uint32_t mc = *reinterpret_cast<const uint32_t*>((uint8_t*)m_ + k);
-                const uint32_t vc = *reinterpret_cast<const uint32_t*>((uint8_t*)v_ + k);
+                const uint32_t mc = next_m[j][tid], vc = next_v[j][tid];
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     m[j][i] = decode_m(mc, 2 * i, {ms, ms});
@@ -236,6 +297,7 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
                 for (int i = 0; i < H; ++i) m[j][i] = two_at(mp, i), v[j][i] = two_at(vp, i);
             }
         }
+        if (b < tab.blocks) next = find(b);
         float mbig = 0.f, vbig = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -298,7 +360,7 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
             const int me = block_exponent(mtop), ve = block_exponent(vtop);
             const float mi = __uint_as_float((uint32_t)(127 - me) << 23);
             const float vi = __uint_as_float((uint32_t)(127 - ve) << 23);
-            const uint32_t key = mix32(e.key + (uint32_t)((uint64_t)first >> 32));
+            const uint32_t key = mix32(e.key + (uint32_t)((uint64_t)e.first >> 32));
             const Two<float> mi2{mi, mi}, vi2{vi, vi};
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
@@ -309,15 +371,20 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
                     const Two<float> ym =
                         Two<float>{fabsf(x.x), fabsf(x.y)} * mi2 * Two<float>{0x1p-111f, 0x1p-111f};
                     const Two<float> yv = y * vi2 * Two<float>{0x1p-95f, 0x1p-95f};
-                    const uint32_t k = (uint32_t)first + (j * 32 + lane) * V + 2 * i;
-                    const uint32_t h0 = mix32(k ^ key), h1 = mix32((k + 1) ^ key);
-                    auto high = [](uint32_t h) { return (h >> 12 & 0xFFFF0u) | 8u; };
+                    const uint32_t k = (uint32_t)e.first + (j * 32 + lane) * V + 2 * i;
+                    auto mix = [&](uint32_t h) {
+                        h = (h ^ shr(h, a.s16)) * 0x85EBCA6Bu;
+                        h = (h ^ shr(h, a.s13)) * 0xC2B2AE35u;
+                        return h ^ shr(h, a.s16);
+                    };
+                    const uint32_t h0 = mix(k ^ key), h1 = mix((k + 1) ^ key);
+                    auto high = [&](uint32_t h) { return (shr(h, a.s12) & 0xFFFF0u) | 8u; };
                     auto low = [](uint32_t h) { return (h << 4 & 0xFFFF0u) | 8u; };
-                    mc[2 * i] = rounded(ym.x, high(h0));
-                    mc[2 * i + 1] = rounded(ym.y, high(h1));
+                    mc[2 * i] = rounded(ym.x, high(h0), a.s20);
+                    mc[2 * i + 1] = rounded(ym.y, high(h1), a.s20);
                     // a positive v keeps a positive code
-                    vc[2 * i] = max(rounded(yv.x, low(h0)), (int)min(__float_as_uint(y.x), 1u));
-                    vc[2 * i + 1] = max(rounded(yv.y, low(h1)), (int)min(__float_as_uint(y.y), 1u));
+                    vc[2 * i] = max(rounded(yv.x, low(h0), a.s20), (int)min(__float_as_uint(y.x), 1u));
+                    vc[2 * i + 1] = max(rounded(yv.y, low(h1), a.s20), (int)min(__float_as_uint(y.y), 1u));
                 }
                 const int64_t k = at + (j * 32 + lane) * V;
                 if constexpr (V == 4) {
@@ -328,8 +395,8 @@ adamw_kernel(const __grid_constant__ AdamwTable tab,
                 }
             }
             if (lane == 0) {
-                m_exp[b] = mtop >= 0x7F800000u ? 255 : (uint8_t)(me + 128);
-                v_exp[b] = vtop >= 0x7F800000u ? 255 : (uint8_t)(ve + 128);
+                m_exp[block] = mtop >= 0x7F800000u ? 255 : (uint8_t)(me + 128);
+                v_exp[block] = vtop >= 0x7F800000u ? 255 : (uint8_t)(ve + 128);
             }
         } else {
 #pragma unroll
@@ -367,17 +434,6 @@ adamw_values_kernel(int64_t quads, const uint32_t* __restrict__ mc,
     }
 }
 
-int resident_ctas(const void* kernel) {
-    int each = 0, dev = 0, sms = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&each, kernel, 32 * kWarps, 0) !=
-            cudaSuccess ||
-        cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        each * sms <= 0)
-        return 152 * 4;
-    return each * sms;
-}
-
 template <typename P, typename G, bool EIGHT>
 cudaError_t launch(const AdamwTable& tab, const AdamwCall& c, int64_t block0, cudaStream_t s) {
     using C = typename Compute<P>::type;
@@ -385,17 +441,18 @@ cudaError_t launch(const AdamwTable& tab, const AdamwCall& c, int64_t block0, cu
     const double bc2 = 1.0 - std::pow(c.beta2, (double)c.step);
     const AdamwScalars<C> a{(C)c.beta1, (C)(1.0 - c.beta1), (C)c.beta2, (C)(1.0 - c.beta2),
                             (C)(1.0 - c.lr * c.weight_decay), (C)(c.lr / bc1),
-                            (C)(1.0 / std::sqrt(bc2)), (C)c.eps};
+                            (C)(1.0 / std::sqrt(bc2)), (C)c.eps, 1u << 16, 1u << 19, 1u << 12,
+                            1u << 20};
     const size_t each = EIGHT ? 1 : sizeof(C);
     const int64_t at = block0 * kBlock;
     const int64_t ctas = ((int64_t)tab.blocks + kWarps - 1) / kWarps;
-    // 8-bit states are bound by arithmetic as much as by HBM: as many CTAs as are
-    // resident at once, for a last wave that fills 0.6 of the SMs cost a fifth.
-    // With 32-bit ones two and two thirds of a wave measured best (968 us against
-    // 1000 us for 240 M parameters).
-    static const int resident =
-        EIGHT ? resident_ctas((const void*)adamw_kernel<P, G, EIGHT>) : 152 * 8;
-    const unsigned grid = (unsigned)std::min<int64_t>(ctas, resident);
+    // A few blocks a warp and not more: SMs differ in speed, and new CTAs go where
+    // one ends.  239 M parameters with 8-bit states took 668 us with 8 blocks a warp,
+    // 718 us with 4 or 24, 800 us in one wave; with 32-bit ones 944 us with 4, 951 us
+    // with 8 and 977 us in one wave.
+    constexpr int kRounds = EIGHT ? 8 : 4;
+    const int64_t most = ((int64_t)tab.blocks + kRounds * kWarps - 1) / (kRounds * kWarps);
+    const unsigned grid = (unsigned)std::min<int64_t>(ctas, std::max<int64_t>(most, 152 * 4));
     adamw_kernel<P, G, EIGHT><<<grid, 32 * kWarps, 0, s>>>(
         tab, a, (uint8_t*)c.m + at * each, (uint8_t*)c.v + at * each,
         EIGHT ? c.m_exp + block0 : nullptr, EIGHT ? c.v_exp + block0 : nullptr,

@@ -133,7 +133,8 @@ constexpr int kNormForwardCtas = 152 * 8, kNormBackwardCtas = 152 * 8;
 struct NormIrrep {
     int l, mul, off, ch;        // first element of a row, first channel
     int T, K;                   // threads of a pair, vectors of a thread (0: read again)
-    int cta0, ctas, max_ctas;   // this launch's CTAs; the most, by the irrep's share of a row
+    int cta0, ctas;             // this launch's CTAs
+    int share, max_ctas;        // of kNorm...Ctas by the time of a pair; the most, whatever the launch
     int64_t part0;              // first element in the gradient's partial rows
 };
 struct NormTable {

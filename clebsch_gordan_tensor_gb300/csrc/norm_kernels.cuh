@@ -1210,7 +1210,7 @@ int shape_table(NormTable& tab, int64_t n, int threads, int of_all, int all, int
         NormIrrep& ir = tab.ir[i];
         if (ir.K == 0) ir.T = threads;
         const int64_t G = threads / ir.T;
-        const int most_ctas = std::max(1, ir.max_ctas * of_all / all);
+        const int most_ctas = std::min(ir.max_ctas, std::max(1, ir.share * of_all / all));
         ir.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(most_ctas, (n + G - 1) / G));
         ir.cta0 = tab.ctas;
         tab.ctas += ir.ctas;
@@ -1327,7 +1327,7 @@ bool rows_apply(NormTable& tab, const Args& a, int& threads, int& K, bool& warp)
         // the shares of row kernels' CTAs, which take more of an SM
         const int most_ctas = std::min(
             ir.max_ctas,
-            std::max(1, ir.max_ctas * Args::kRowCtas / Args::kCtas * kRowThreads / threads));
+            std::max(1, ir.share * Args::kRowCtas / Args::kCtas * kRowThreads / threads));
         ir.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(most_ctas, (a.n + G - 1) / G));
         ir.cta0 = tab.ctas;
         tab.ctas += ir.ctas;

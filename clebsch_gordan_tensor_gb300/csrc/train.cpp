@@ -77,12 +77,12 @@ static bool irrep_tables(cgtp_norm_s& h, const std::vector<Irrep>& irreps) {
         // a share of the CTAs by a pair's time: its elements, and two components'
         // worth for what a pair costs whatever its width
         const int64_t cost = (int64_t)ir.mul * (2 * ir.l + 3), all = h.dim + 2 * h.channels;
-        e.max_ctas = (int)std::max<int64_t>(1, kNormForwardCtas * cost / all);
+        e.share = e.max_ctas = (int)std::max<int64_t>(1, kNormForwardCtas * cost / all);
         h.forward.ir[i] = e;
         // no more partial rows than 64 MB hold, unless that leaves SMs idle
         const int64_t held = ((int64_t)64 << 20) / (2 * (int64_t)ir.mul * 8);
-        e.max_ctas = (int)std::max<int64_t>(
-            1, std::min(kNormBackwardCtas * cost / all, std::max<int64_t>(held, 152)));
+        e.share = (int)std::max<int64_t>(1, kNormBackwardCtas * cost / all);
+        e.max_ctas = (int)std::min<int64_t>(e.share, std::max<int64_t>(held, 304));
         e.part0 = part;
         part += (int64_t)e.max_ctas * 2 * ir.mul;
         h.backward.ir[i] = e;
