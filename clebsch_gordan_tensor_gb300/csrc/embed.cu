@@ -698,7 +698,7 @@ cudaError_t forward_v(const EmbedCall& c, cudaStream_t s) {
     const int T = lanes_for((c.d + V - 1) / V);
     const bool long_rows = c.d > (int64_t)T * V;
     const int64_t groups = long_rows ? c.n : (c.n + 3) / 4;
-    const unsigned grid = (unsigned)std::min<int64_t>((groups + 256 / T - 1) / (256 / T), 152 * 16);
+    const unsigned grid = (unsigned)std::min<int64_t>((groups + 256 / T - 1) / (256 / T), 152 * 32);
     auto kernel = long_rows ? embed_forward_kernel<S, I, V, true>
                             : embed_forward_kernel<S, I, V, false>;
     kernel<<<grid, 256, 0, s>>>(c.n, c.v, c.d, T, (const I*)c.index, (const S*)c.in, (C)c.scale,
