@@ -52,6 +52,17 @@ constexpr int kWidth = V == 8 && L > 1 ? 4 : V;
 // pair still fits a few warps and has as much in flight.
 template <int V, int L>
 constexpr int kEach = V > 1 ? 1 : L <= 3 ? 4 : 2;
+// Threads of a group, where the launch's groups all have TC (0: any number).
+// With single elements an address costs as much as the arithmetic on what is
+// there: a constant group leaves a thread's elements at constant distances.
+// Residual without / with, 16,384 x 4001 bf16: 291 / 246 us, 65,536 x 1001 bf16:
+// 310 / 225 us, its gradient 853 / 727 us, 100,000 x (65x0e+65x1o) bf16: 150 / 137.
+// Groups of fewer threads stay at their size: 1001 channels on 512 threads
+// instead of 256 took 465 us.
+template <int TC>
+__device__ __forceinline__ int group_of(const NormIrrep& ir) {
+    return TC ? TC : ir.T;
+}
 
 __device__ __forceinline__ float rsqrt_of(float x) { return rsqrtf(x); }
 __device__ __forceinline__ double rsqrt_of(double x) { return 1.0 / sqrt(x); }
@@ -128,17 +139,18 @@ struct ForwardRegs {
     }
 };
 
-template <typename S, int V, int L, int K>
+template <int TC, typename S, int V, int L, int K>
 __device__ __forceinline__ void load_forward(ForwardRegs<S, V, L, K>& q, const NormIrrep& ir,
                                              const NormForward& a, int64_t row, int t) {
     if (row >= a.n) return;
+    const int T = group_of<TC>(ir);
     const S* b = row_of<const S>(a.b, row, ir.off);
     const S* x = row_of<const S>(a.x, row, ir.off);
     const S* z = row_of<const S>(a.gate, row, ir.ch);
 #pragma unroll
     for (int k = 0; k < K; ++k)
-        if (t + k * ir.T < ir.mul / V) {
-            const int u = (t + k * ir.T) * V;
+        if (t + k * T < ir.mul / V) {
+            const int u = (t + k * T) * V;
 #pragma unroll
             for (int m = 0; m < 2 * L + 1; ++m) {
                 q.b[k][m] = load_pack<S, V>(b + m * ir.mul + u);
@@ -148,12 +160,12 @@ __device__ __forceinline__ void load_forward(ForwardRegs<S, V, L, K>& q, const N
         }
 }
 
-template <typename S, int V, int L, int K>
+template <int TC, typename S, int V, int L, int K>
 __device__ __forceinline__ void forward_body(const NormIrrep& ir, int cta, const NormForward& a,
                                              typename Compute<S>::type (*sums)[kMaxWarps]) {
     using C = typename Compute<S>::type;
     constexpr int M = 2 * L + 1;
-    const int T = ir.T, t = threadIdx.x % T, G = blockDim.x / T;
+    const int T = group_of<TC>(ir), t = threadIdx.x % T, G = blockDim.x / T;
     const int U = ir.mul / V;
     const C inv_d = (C)1 / (C)(M * ir.mul), eps = (C)a.eps;
     const C *w = (const C*)a.weight, *sc = (const C*)a.scale, *w2 = (const C*)a.next_weight;
@@ -172,9 +184,9 @@ __device__ __forceinline__ void forward_body(const NormIrrep& ir, int cta, const
     // scalar rows are short: the next one is on its way during the sums
     constexpr bool kAhead = L == 0 && K * V <= 8;
     ForwardRegs<S, V, L, K> q, ahead;
-    load_forward(q, ir, a, row, t);
+    load_forward<TC>(q, ir, a, row, t);
     for (int64_t base = (int64_t)cta * G; base < a.n; base += step, row += step) {
-        if constexpr (kAhead) load_forward(ahead, ir, a, row + step, t);
+        if constexpr (kAhead) load_forward<TC>(ahead, ir, a, row + step, t);
         const bool in = row < a.n;
         C s[1] = {0};
 #pragma unroll
@@ -226,7 +238,7 @@ __device__ __forceinline__ void forward_body(const NormIrrep& ir, int cta, const
         if constexpr (kAhead)
             q = ahead;
         else
-            load_forward(q, ir, a, row + step, t);
+            load_forward<TC>(q, ir, a, row + step, t);
     }
 }
 
@@ -330,7 +342,7 @@ __device__ void forward_wide(const NormIrrep& ir, int cta, const NormForward& a,
 template <int LC, int K>
 constexpr int kForwardCtas = LC == 0 && K == 1 ? 2 : 1;
 
-template <typename S, int V, int LC, int K>
+template <typename S, int V, int LC, int K, int TC>
 __global__ void __launch_bounds__(LC == 0 ? 512 : 256, (kForwardCtas<LC, K>))
 norm_forward_kernel(const __grid_constant__ NormTable tab, const __grid_constant__ NormForward a) {
     __shared__ typename Compute<S>::type sums[6][kMaxWarps];
@@ -338,7 +350,7 @@ norm_forward_kernel(const __grid_constant__ NormTable tab, const __grid_constant
     while (i + 1 < tab.n && (int)blockIdx.x >= tab.ir[i + 1].cta0) ++i;
     const NormIrrep& ir = tab.ir[i];
     const int cta = blockIdx.x - ir.cta0;
-#define CALL(L, K) forward_body<S, kWidth<V, L>, L, K>(ir, cta, a, sums)
+#define CALL(L, K) forward_body<TC, S, kWidth<V, L>, L, K>(ir, cta, a, sums)
     CGTP_NORM_BODIES(LC, V, K, CALL, (forward_wide<S, V>(ir, cta, a, sums)))
 #undef CALL
 }
@@ -366,21 +378,22 @@ struct BackwardRegs {
     }
 };
 
-template <typename S, int V, int L, int K>
+template <int TC, typename S, int V, int L, int K>
 __device__ __forceinline__ void load_backward(BackwardRegs<S, V, L, K>& q, const NormIrrep& ir,
                                               const NormBackward& a, int64_t row, int t) {
     if (row >= a.n) {  // adds nothing to the channel sums
         q = BackwardRegs<S, V, L, K>();
         return;
     }
+    const int T = group_of<TC>(ir);
     const S *b = row_of<const S>(a.b, row, ir.off), *h = row_of<const S>(a.h, row, ir.off);
     const S *gh = row_of<const S>(a.grad_h, row, ir.off);
     const S *gy = row_of<const S>(a.grad_y, row, ir.off);
     const S* z = row_of<const S>(a.gate, row, ir.ch);
 #pragma unroll
     for (int k = 0; k < K; ++k)
-        if (t + k * ir.T < ir.mul / V) {
-            const int u = (t + k * ir.T) * V;
+        if (t + k * T < ir.mul / V) {
+            const int u = (t + k * T) * V;
 #pragma unroll
             for (int m = 0; m < 2 * L + 1; ++m) {
                 q.b[k][m] = load_pack<S, V>(b + m * ir.mul + u);
@@ -422,7 +435,7 @@ struct BackwardRing {
         }
     }
     __device__ __forceinline__ void fetch(const NormIrrep& ir, const NormBackward& a, int64_t row,
-                                          int t) {
+                                          int t, int T) {
         if (row < a.n) {
             const S *b = row_of<const S>(a.b, row, ir.off), *h = row_of<const S>(a.h, row, ir.off);
             const S *gh = row_of<const S>(a.grad_h, row, ir.off);
@@ -433,8 +446,8 @@ struct BackwardRing {
             };
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (t + k * ir.T < ir.mul / V) {
-                    const int u = (t + k * ir.T) * V;
+                if (t + k * T < ir.mul / V) {
+                    const int u = (t + k * T) * V;
 #pragma unroll
                     for (int m = 0; m < M; ++m) {
                         get(0, k, m, b + m * ir.mul + u);
@@ -473,13 +486,13 @@ constexpr int kRingBytes =
         ? 0
         : (4 * (2 * L + 1) + 1) * kEach<V, L> * kWidth<V, L> * (int)sizeof(S);
 
-template <typename S, int V, int L, int K>
+template <int TC, typename S, int V, int L, int K>
 __device__ __forceinline__ void backward_body(const NormIrrep& ir, int cta, const NormBackward& a,
                                               typename Compute<S>::type (*sums)[kMaxWarps],
                                               unsigned char* dynamic) {
     using C = typename Compute<S>::type;
     constexpr int M = 2 * L + 1;
-    const int T = ir.T, t = threadIdx.x % T, G = blockDim.x / T;
+    const int T = group_of<TC>(ir), t = threadIdx.x % T, G = blockDim.x / T;
     const int U = ir.mul / V;
     const C inv_d = (C)1 / (C)(M * ir.mul), eps = (C)a.eps;
     C ws[K][V], w2[K][V], acc_a[K][V], acc_q[K][V];
@@ -509,15 +522,15 @@ __device__ __forceinline__ void backward_body(const NormIrrep& ir, int cta, cons
     using Ring = std::conditional_t<kRing, BackwardRing<S, V, L, K>, None>;
     Ring ring(dynamic);
     if constexpr (kRing)
-        ring.fetch(ir, a, row, t);
+        ring.fetch(ir, a, row, t, T);
     else
-        load_backward(q, ir, a, row, t);
+        load_backward<TC>(q, ir, a, row, t);
     for (int64_t base = (int64_t)cta * G; base < a.n; base += step, row += step) {
-        if constexpr (kAhead) load_backward(ahead, ir, a, row + step, t);
+        if constexpr (kAhead) load_backward<TC>(ahead, ir, a, row + step, t);
         const bool in = row < a.n;
         if constexpr (kRing) {
             ring.read(q, in);
-            ring.fetch(ir, a, row + step, t);
+            ring.fetch(ir, a, row + step, t, T);
         }
         C s[3] = {0, 0, 0};  // b^2, h^2, next_weight gy h
 #pragma unroll
@@ -602,7 +615,7 @@ __device__ __forceinline__ void backward_body(const NormIrrep& ir, int cta, cons
         if constexpr (kAhead)
             q = ahead;
         else if constexpr (!kRing)
-            load_backward(q, ir, a, row + step, t);
+            load_backward<TC>(q, ir, a, row + step, t);
     }
     if constexpr (kRing) copies_wait<0>();
     if (!a.partial) return;
@@ -740,7 +753,7 @@ __device__ void backward_wide(const NormIrrep& ir, int cta, const NormBackward& 
     }
 }
 
-template <typename S, int V, int LC, int K>
+template <typename S, int V, int LC, int K, int TC>
 __global__ void __launch_bounds__(LC == 0 ? 512 : 128, LC == 3 ? 3 : 1)
 norm_backward_kernel(const __grid_constant__ NormTable tab,
                      const __grid_constant__ NormBackward a) {
@@ -751,7 +764,7 @@ norm_backward_kernel(const __grid_constant__ NormTable tab,
     while (i + 1 < tab.n && (int)blockIdx.x >= tab.ir[i + 1].cta0) ++i;
     const NormIrrep& ir = tab.ir[i];
     const int cta = blockIdx.x - ir.cta0;
-#define CALL(L, K) backward_body<S, kWidth<V, L>, L, K>(ir, cta, a, sums, dynamic)
+#define CALL(L, K) backward_body<TC, S, kWidth<V, L>, L, K>(ir, cta, a, sums, dynamic)
     CGTP_NORM_BODIES(LC, V, K, CALL, (backward_wide<S, V>(ir, cta, a, sums)))
 #undef CALL
 }
@@ -1242,14 +1255,14 @@ cudaError_t finish(const NormTable& tab, const NormBackward& a, cudaStream_t s) 
                           s, tab, a);
 }
 
-template <typename S, int V, int LC, int K>
+template <typename S, int V, int LC, int K, int TC = 0>
 cudaError_t launch(const NormTable& tab, int threads, const NormForward& a, cudaStream_t s) {
-    norm_forward_kernel<S, V, LC, K><<<tab.ctas, threads, 0, s>>>(tab, a);
+    norm_forward_kernel<S, V, LC, K, TC><<<tab.ctas, threads, 0, s>>>(tab, a);
     count_launch();
     return cudaGetLastError();
 }
 
-template <typename S, int V, int LC, int K>
+template <typename S, int V, int LC, int K, int TC = 0>
 cudaError_t launch(const NormTable& tab, int threads, const NormBackward& a, cudaStream_t s) {
     using C = typename Compute<S>::type;
     // one set of channel sums of every thread, and before that the rows ahead
@@ -1267,10 +1280,10 @@ cudaError_t launch(const NormTable& tab, int threads, const NormBackward& a, cud
     const int smem = threads * each;
     if (smem > 48 << 10) {
         static std::atomic<uint32_t> done{0};
-        const cudaError_t e = allow_smem((const void*)norm_backward_kernel<S, V, LC, K>, done);
+        const cudaError_t e = allow_smem((const void*)norm_backward_kernel<S, V, LC, K, TC>, done);
         if (e != cudaSuccess) return e;
     }
-    norm_backward_kernel<S, V, LC, K><<<tab.ctas, threads, smem, s>>>(tab, a);
+    norm_backward_kernel<S, V, LC, K, TC><<<tab.ctas, threads, smem, s>>>(tab, a);
     count_launch();
     const cudaError_t e = cudaGetLastError();
     return e != cudaSuccess ? e : finish<C>(tab, a, s);
@@ -1353,18 +1366,36 @@ cudaError_t launch_v(NormTable tab, const Args& a, cudaStream_t s) {
         if (rows_apply<S>(tab, a, threads, k, warp)) return launch_rows<S>(tab, threads, k, warp, a, s);
     }
     const int threads = shape_table<V>(tab, a.n, Args::kThreads, Args::kBodyCtas, Args::kCtas, k, l);
-    constexpr int least = V > 1 ? 1 : 4;
-    if (l > 3) return launch<S, V, 6, least>(tab, threads, a, s);
-    // past the row kernels eight 16-bit channels leave the body that reads again
-    if (l > 0 || V == 8) return launch<S, V, 3, least>(tab, threads, a, s);
-    if constexpr (V < 8) {
-        if constexpr (!rows) {
-            if (k == least) return launch<S, V, 0, least>(tab, threads, a, s);
-            if (k == 2 * least) return launch<S, V, 0, 2 * least>(tab, threads, a, s);
+    if constexpr (V == 1) {
+        int T = tab.ir[0].T;  // of all groups, or 0
+        for (int i = 0; i < tab.n; ++i) T = tab.ir[i].T == T && tab.ir[i].K ? T : 0;
+        if (l > 3) return launch<S, 1, 6, 4>(tab, threads, a, s);
+        if (l > 0) return T == 32 ? launch<S, 1, 3, 4, 32>(tab, threads, a, s)
+                                  : launch<S, 1, 3, 4>(tab, threads, a, s);
+        if (k == 4 && T == 32) return launch<S, 1, 0, 4, 32>(tab, threads, a, s);
+        if (k == 4 && T == 64) return launch<S, 1, 0, 4, 64>(tab, threads, a, s);
+        if (k == 4 && T == 128) return launch<S, 1, 0, 4, 128>(tab, threads, a, s);
+        if (k == 4 && T == 256) return launch<S, 1, 0, 4, 256>(tab, threads, a, s);
+        if (k == 4 && T == 512) return launch<S, 1, 0, 4, 512>(tab, threads, a, s);
+        if (k == 8 && T == 512) return launch<S, 1, 0, 8, 512>(tab, threads, a, s);
+        if (k == 16 && T == 512) return launch<S, 1, 0, 16, 512>(tab, threads, a, s);
+        // several widths, 64 channels or fewer, or past 8192
+        if (k == 4) return launch<S, 1, 0, 4>(tab, threads, a, s);
+        if (k == 8) return launch<S, 1, 0, 8>(tab, threads, a, s);
+        return launch<S, 1, 0, 16>(tab, threads, a, s);
+    } else {
+        if (l > 3) return launch<S, V, 6, 1>(tab, threads, a, s);
+        // past the row kernels eight 16-bit channels leave the body that reads again
+        if (l > 0 || V == 8) return launch<S, V, 3, 1>(tab, threads, a, s);
+        if constexpr (V < 8) {
+            if constexpr (!rows) {
+                if (k == 1) return launch<S, V, 0, 1>(tab, threads, a, s);
+                if (k == 2) return launch<S, V, 0, 2>(tab, threads, a, s);
+            }
+            return launch<S, V, 0, 4>(tab, threads, a, s);
         }
-        return launch<S, V, 0, 4 * least>(tab, threads, a, s);
+        return cudaErrorInvalidValue;  // not reached
     }
-    return cudaErrorInvalidValue;  // not reached
 }
 
 template <typename S, typename Args>
