@@ -22,9 +22,9 @@
 // 2^-18, lies below sqrt of the smallest v, so no element's m / sqrt(v) is
 // blown up by the formats.
 //
-// Bounds: with 32-bit states HBM (239 M fp32 parameters in 968 us, 28 bytes each:
-// 6.9 TB/s); with 8-bit ones the integer pipe (two thirds busy) and issue as much
-// as HBM (805 us, 18 bytes each with a 16-bit copy).
+// Bounds: with 32-bit states HBM (239 M fp32 parameters in 944 us, 28 bytes each:
+// 7.1 TB/s); with 8-bit ones the instructions of packing and rounding as much as
+// HBM (668 us, 18 bytes each with a 16-bit copy: 6.4 TB/s).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -12,12 +12,13 @@
 // values: the same inputs give the same bits.
 //
 // Both directions are bound by HBM once they are large: 131,072 rows of 1024
-// bfloat16 are copied in 49 us (95% of a copy's bandwidth) and summed in 48-53 us,
-// with 20 us of sort and 12 us of join around the sums, chains of L2 latencies
-// that the launches' overlap hides in part (89 us in all).
+// bfloat16 are copied in 47 us (a copy's bandwidth) and summed in 48-53 us, with
+// 20 us of sort and 12 us of join around the sums, chains of L2 latencies that the
+// launches' overlap hides in part (90 us in all).
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.hpp"
 #include "storage.cuh"
@@ -31,7 +32,8 @@ namespace {
 // ------------------------------------------------------------- lookup --
 
 // A group of T lanes copies R = 4 vectors a lane at a time: of four rows where a
-// row fits the lanes (Long false), of one row where it does not.  No division:
+// row fits the lanes (Long false), of one row where it does not (eight of 4 bytes;
+// of single 16-bit elements four, 76 us against 88 with sixteen for 60,000 x 1001).  No division:
 // with a tile number computed for every vector the copy of 131,072 x 1024 bf16
 // rows was bound by its instructions (74 us).
 template <typename S, typename I, int V, bool Long>
@@ -40,7 +42,7 @@ embed_forward_kernel(int64_t n, int64_t v, int64_t d, int T, const I* __restrict
                      const S* __restrict__ table, typename Compute<S>::type scale,
                      S* __restrict__ out, int64_t stride) {
     using C = typename Compute<S>::type;
-    constexpr int R = 4;
+    constexpr int R = Long && V * sizeof(S) == 4 ? 8 : 4;
     const int64_t groups = (int64_t)gridDim.x * (256 / T);
     const int64_t group = (int64_t)blockIdx.x * (256 / T) + threadIdx.x / T;
     const int col0 = threadIdx.x % T * V;
@@ -600,9 +602,10 @@ cudaError_t sort_pass(const EmbedCall& c, const Layout& L, int shift, const I* i
 }
 
 // V: elements of an access; J: sums of one in the join.
-template <typename S, int V, int J>
+template <typename S, int V>
 cudaError_t backward_v(const EmbedCall& c, const Layout& L, int sorted, cudaStream_t s) {
     using C = typename Compute<S>::type;
+    constexpr int J = std::min(V, 4);
     uint8_t* ws = (uint8_t*)c.ws;
     const uint32_t* keys = (const uint32_t*)(ws + L.keys[sorted]);
     const uint32_t* pos = (const uint32_t*)(ws + L.pos[sorted]);
@@ -627,12 +630,30 @@ cudaError_t backward_v(const EmbedCall& c, const Layout& L, int sorted, cudaStre
                           (const C*)(ws + L.partial), list);
 }
 
-// Rows that can move in 16-byte accesses.
+// Elements of the widest access, 16 bytes at most, that fits every row.  Accesses
+// of 8 and 4 bytes besides 16 and single elements: 60,000 x 1002 bf16 copied in 43
+// instead of 76 us and added up in 82 instead of 108, 10,634 x 1854 fp32 in 29 (38)
+// and 95 (107).
 template <typename S>
-bool wide(const EmbedCall& c) {
-    constexpr int V = 16 / sizeof(S);
-    return c.d % V == 0 && c.in_stride % V == 0 && c.out_stride % V == 0 &&
-           (uintptr_t)c.in % 16 == 0 && (uintptr_t)c.out % 16 == 0;
+int access_of(const EmbedCall& c) {
+    const uint64_t bits = (uint64_t)(c.d | c.in_stride | c.out_stride) * sizeof(S) |
+                          (uintptr_t)c.in | (uintptr_t)c.out;
+    int V = 16 / sizeof(S);
+    while (V > 1 && bits % (V * sizeof(S)) != 0) V /= 2;
+    return V;
+}
+
+// f of that number as a constant.
+template <typename S, typename F>
+cudaError_t with_access(const EmbedCall& c, F f) {
+    constexpr int most = 16 / sizeof(S);
+    const int V = access_of<S>(c);
+    if (V == most) return f(std::integral_constant<int, most>{});
+    if constexpr (most > 2)
+        if (V == most / 2) return f(std::integral_constant<int, most / 2>{});
+    if constexpr (most > 4)
+        if (V == most / 4) return f(std::integral_constant<int, most / 4>{});
+    return f(std::integral_constant<int, 1>{});
 }
 
 template <typename S, typename I, int V>
@@ -659,12 +680,11 @@ bool small(int64_t n, int64_t v, int64_t d, int64_t V) {
 template <typename S>
 cudaError_t backward(const EmbedCall& c, cudaStream_t s) {
     cudaError_t e;
-    if (c.n > 0 && small(c.n, c.v, c.d, wide<S>(c) ? 16 / sizeof(S) : 1)) {
-        constexpr int V = 16 / sizeof(S);
-        if (c.index_bits == 32)
-            return wide<S>(c) ? small_v<S, int32_t, V>(c, s) : small_v<S, int32_t, 1>(c, s);
-        return wide<S>(c) ? small_v<S, int64_t, V>(c, s) : small_v<S, int64_t, 1>(c, s);
-    }
+    if (c.n > 0 && small(c.n, c.v, c.d, access_of<S>(c)))
+        return with_access<S>(c, [&](auto V) {
+            return c.index_bits == 32 ? small_v<S, int32_t, V()>(c, s)
+                                      : small_v<S, int64_t, V()>(c, s);
+        });
     if (c.n == 0) {
         const int64_t bytes = c.v * c.d * (int64_t)sizeof(S);
         const unsigned grid = (unsigned)std::min<int64_t>(bytes / 4096 + 1, 152 * 16);
@@ -687,9 +707,7 @@ cudaError_t backward(const EmbedCall& c, cudaStream_t s) {
                           (const uint32_t*)(ws + L.pos[to ^ 1]), to, s);
         if (e != cudaSuccess) return e;
     }
-    constexpr int V = 16 / sizeof(S), J = sizeof(S) == 8 ? 2 : 4;
-    return wide<S>(c) ? backward_v<S, V, J>(c, L, to ^ 1, s)
-                      : backward_v<S, 1, 1>(c, L, to ^ 1, s);
+    return with_access<S>(c, [&](auto V) { return backward_v<S, V()>(c, L, to ^ 1, s); });
 }
 
 template <typename S, typename I, int V>
@@ -698,6 +716,7 @@ cudaError_t forward_v(const EmbedCall& c, cudaStream_t s) {
     const int T = lanes_for((c.d + V - 1) / V);
     const bool long_rows = c.d > (int64_t)T * V;
     const int64_t groups = long_rows ? c.n : (c.n + 3) / 4;
+    // 131,072 x 1024 bf16: 47.3 us with up to 32 CTAs an SM, 48.9 with 16
     const unsigned grid = (unsigned)std::min<int64_t>((groups + 256 / T - 1) / (256 / T), 152 * 32);
     auto kernel = long_rows ? embed_forward_kernel<S, I, V, true>
                             : embed_forward_kernel<S, I, V, false>;
@@ -709,10 +728,10 @@ cudaError_t forward_v(const EmbedCall& c, cudaStream_t s) {
 
 template <typename S>
 cudaError_t forward(const EmbedCall& c, cudaStream_t s) {
-    constexpr int V = 16 / sizeof(S);
-    if (c.index_bits == 32)
-        return wide<S>(c) ? forward_v<S, int32_t, V>(c, s) : forward_v<S, int32_t, 1>(c, s);
-    return wide<S>(c) ? forward_v<S, int64_t, V>(c, s) : forward_v<S, int64_t, 1>(c, s);
+    return with_access<S>(c, [&](auto V) {
+        return c.index_bits == 32 ? forward_v<S, int32_t, V()>(c, s)
+                                  : forward_v<S, int64_t, V()>(c, s);
+    });
 }
 
 }  // namespace

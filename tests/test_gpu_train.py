@@ -659,3 +659,35 @@ def test_binding_refusals():
             f()
             pytest.fail(f"call {k} was not refused")
     assert opt.step_count == 0
+
+
+# ------------------------------------------ rows of every width of access --
+
+ACCESS_EMBED = [  # n, v, d, pad, shift: accesses of 16, 8, 4 and 2 bytes in both directions
+    (2500, 30, 1004, 0, 0), (2500, 30, 1002, 0, 0), (2500, 30, 1001, 0, 0), (2100, 500, 34, 0, 0),
+    (1500, 40, 36, 8, 4), (1500, 40, 40, 6, 2), (400, 10, 78, 2, 0), (400, 10, 140, 4, 0),
+    (400, 10, 140, 4, 2), (1, 3, 2, 0, 0), (33, 9, 514, 0, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=name)
+@pytest.mark.parametrize("case", ACCESS_EMBED, ids=lambda c: "-".join(map(str, c)))
+def test_embed_rows_of_every_alignment(case, dtype):
+    test_embed_forward(case, dtype)
+    test_embed_backward(case, dtype)
+
+
+ACCESS_NORM = [  # n, irreps, pad, shift: single elements, groups of each size
+    (37, "65x0e", 0, 0), (3000, "101x0e", 0, 0), (37, "131x0e", 0, 0), (2100, "257x0e", 0, 0),
+    (700, "777x0e", 0, 0), (300, "1501x0e", 0, 0), (9, "3001x0e", 0, 0), (200, "4001x0e", 0, 0),
+    (9, "8001x0e", 0, 0), (9, "8192x0e", 3, 1), (600, "128x0e", 3, 1), (9, "33x0e+101x0o", 0, 0),
+    (9, "3001x0e+5x0o", 0, 0), (900, "67x0e+67x1o+67x2e", 0, 0), (9, "128x0e+65x1o+97x3o", 0, 0),
+    (9, "67x0e+33x1o", 0, 0), (9, "67x0e+9001x0o", 0, 0), (9, "67x0e+300x1o", 0, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=name)
+@pytest.mark.parametrize("case", ACCESS_NORM, ids=lambda c: f"{c[0]}-{c[1]}-{c[2]}-{c[3]}")
+def test_norm_rows_of_every_group_size(case, dtype):
+    test_norm(case, dtype)
+    test_residual(case, dtype)
