@@ -101,9 +101,16 @@ __device__ __forceinline__ Two<float> decode_v(uint32_t four, int i, Two<float> 
     auto value = [&](int k) { return __uint_as_float(shifted(four, 20 - 8 * k) & 0x0FF00000u); };
     return Two<float>{value(i), value(i + 1)} * Two<float>{0x1p95f, 0x1p95f} * scale;
 }
+// x >> (32 - log2 by) on the multiply pipe: by is a power of two that the compiler
+// does not know.
+__device__ __forceinline__ uint32_t shr(uint32_t x, uint32_t by) {
+    uint32_t r;
+    asm("mul.hi.u32 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(by));
+    return r;
+}
+
 // y, the fp32 bits of a scaled magnitude, with the noise below the last bit kept
 // added: the code, but for the clamp at the largest one.
-__device__ __forceinline__ uint32_t shr(uint32_t x, uint32_t by);
 __device__ __forceinline__ int rounded(float y, uint32_t noise, uint32_t by) {
     return (int)shr(__float_as_uint(y) + noise, by);
 }
@@ -137,14 +144,6 @@ __device__ __forceinline__ uint32_t signs(Two<float> a, Two<float> b) {
 __device__ __forceinline__ float larger(float top, float x) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(top), "f"(fabsf(x)));
-    return r;
-}
-
-// x >> (32 - log2 by) on the multiply pipe: by is a power of two that the compiler
-// does not know.
-__device__ __forceinline__ uint32_t shr(uint32_t x, uint32_t by) {
-    uint32_t r;
-    asm("mul.hi.u32 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(by));
     return r;
 }
 
